@@ -153,15 +153,27 @@ extern "C" {
 #define KV_DEVERR_BLOCK_RANGE 0x1 /* a block table held an id outside [0, num_blocks); that
                                      (layer, kv, page) tile was skipped */
 
+/* element types of the append and attention operators */
+#define KV_TYPE_F16 0  /* IEEE half */
+#define KV_TYPE_BF16 1 /* bfloat16 */
+#define KV_TYPE_E4M3 2 /* 8-bit float, OCP e4m3fn (pools only) */
+
+/* kv_attn_desc.flags */
+#define KV_ATTN_FULL 0x1 /* every query sees every cached token (no causal mask) */
+
 /* kv_ring_create flags */
 #define KV_RING_COHERENT 0x0     /* hipHostMalloc coherent mapped memory (default) */
 #define KV_RING_NONCOHERENT 0x1  /* hipHostMallocNonCoherent: the GPU may cache it */
 
 /* Limits of one call. */
 #define KV_MAX_SPANS 4096
+#define KV_MAX_PAGE_COPIES 65536 /* records of one kv_copy_pages or kv_remap_tables call */
+#define KV_MAX_SEQS 4096         /* sequences of one attention plan */
+#define KV_MAX_ATTN_DIM 256      /* head_dim of the attention operators */
 
 typedef struct kv_pool kv_pool; /* opaque, owned by the library */
 typedef struct kv_ring kv_ring; /* opaque, owned by the library */
+typedef struct kv_attn_plan kv_attn_plan; /* opaque, owned by the library */
 
 typedef struct {
     int32_t num_layers;   /* L >= 1 */
@@ -220,6 +232,61 @@ typedef struct {
     int64_t max_chunk_bytes;/* largest chunk of the call */
 } kv_transfer_info;
 
+/* One page copied to another of the same pool, or moved (kv_pool_plan_compact). */
+typedef struct {
+    int32_t src, dst;  /* block ids */
+    int32_t n_tokens;  /* tokens [0, n_tokens) are copied, 1 .. block_size */
+} kv_page_copy;
+
+/* One sequence of an attention plan.  Its cache holds kv_len tokens, the q_len newest of
+ * them being the call's new tokens: row q_begin + i of the new tokens' arrays is the token
+ * at position kv_len - q_len + i. */
+typedef struct {
+    const int32_t *block_table; /* device array */
+    int64_t table_len;          /* entries in block_table; >= ceil(kv_len / block_size), < 2^31 */
+    int64_t kv_len;             /* cached tokens, new ones included, 0 .. 2^31 - 4097 */
+    int64_t q_begin;            /* first row of its new tokens, >= 0 */
+    int32_t q_len;              /* new tokens, >= 0 */
+    int32_t prefix_len;         /* cached tokens [0, prefix_len) that every query sees, >= 0 */
+} kv_seq;
+
+typedef struct {
+    int32_t num_q_heads; /* query heads, a multiple of the pool's num_heads: query head h reads
+                            the cache's head h / (num_q_heads / num_heads) */
+    int32_t q_type;      /* of q, out and the appended k and v: KV_TYPE_F16 or KV_TYPE_BF16 */
+    int32_t kv_type;     /* of the pool: q_type, or KV_TYPE_E4M3 */
+    int32_t window;      /* > 0: a query sees its own token and the window - 1 before it; 0: all
+                            before it.  KV_ERR_ARG together with KV_ATTN_FULL */
+    int32_t flags;       /* KV_ATTN_* */
+    int32_t max_seqs;    /* sequences of one kv_attn_plan_set, 1 .. KV_MAX_SEQS */
+    int64_t max_tokens;  /* new tokens of one kv_attn_plan_set, 1 .. 2^24 */
+} kv_attn_desc;
+
+/* Strides are in elements and, like the pointers, multiples of 16 bytes; head_dim elements
+ * of one head lie together. */
+typedef struct {
+    const void *k, *v;                      /* device, [n_tokens][num_heads][head_dim], q_type */
+    int64_t k_token_stride, k_head_stride;
+    int64_t v_token_stride, v_head_stride;
+    int64_t n_tokens;                       /* rows the arrays hold */
+    float k_scale, v_scale;                 /* KV_TYPE_E4M3 pools: a pool element stands for its
+                                               value times this (finite, > 0); else unused */
+} kv_append_args;
+
+typedef struct {
+    const void *q;                          /* device, [n_tokens][num_q_heads][head_dim], q_type */
+    void *out;                              /* device, the same shape and type */
+    float *lse;                             /* device, [n_tokens][num_q_heads] packed, or NULL */
+    const float *alibi_slopes;              /* device, [num_q_heads], or NULL */
+    int64_t q_token_stride, q_head_stride;
+    int64_t out_token_stride, out_head_stride;
+    int64_t n_tokens;                       /* rows the arrays hold */
+    float scale;                            /* of the scores; finite */
+    float softcap;                          /* > 0: scores become softcap * tanh(score / softcap);
+                                               0: off */
+    float k_scale, v_scale;                 /* as in kv_append_args */
+} kv_attend_args;
+
 /* ---- pool ------------------------------------------------------------------ */
 
 /* Validates desc and creates a pool handle with a host bitmap of free blocks (one
@@ -245,11 +312,39 @@ KV_API int kv_pool_destroy(kv_pool *pool);
  * pages lie as close together as the pool's fragmentation allows, which makes
  * reloading them faster), or fails with KV_ERR_OOM and allocates nothing.
  * free: ids must be currently allocated and distinct, else KV_ERR_RANGE and
- * nothing is freed. */
+ * nothing is freed.  A block that kv_pool_share_blocks or kv_pool_fork_blocks gave more
+ * references loses one; it is free when its last one goes. */
 KV_API int kv_pool_alloc_blocks(kv_pool *pool, int32_t n, int32_t *out_ids);
 KV_API int kv_pool_free_blocks(kv_pool *pool, int32_t n, const int32_t *ids);
 /* Free blocks left in the allocator (same source as the two calls above). */
 KV_API int kv_pool_free_count(const kv_pool *pool, int64_t *out);
+
+/* References, for requests that share pages.  share: one more reference on each of the n
+ * ids, which must be allocated (else KV_ERR_RANGE, nothing changed); an id may be listed
+ * twice and then gains two.  block_refs: the references of one block, 0 if it is free.
+ * Host only, like the allocator.  No passage: the pages share prefixes but print no
+ * bookkeeping for it. */
+KV_API int kv_pool_share_blocks(kv_pool *pool, int32_t n, const int32_t *ids);
+KV_API int kv_pool_block_refs(const kv_pool *pool, int32_t id, int32_t *out);
+
+/* Forks a request of n_tokens tokens in blocks ids[0 .. ceil(n_tokens / block_size)):
+ * writes the child's block ids to child_ids (as many).  Whole pages are shared (one more
+ * reference each); a partly filled last page gets a fresh block, and *tail is set to the
+ * copy that fills it (tail->n_tokens is 0 when there is none), for the caller to pass to
+ * kv_copy_pages, the tails of many forks in one call.  ids must be allocated and distinct
+ * (KV_ERR_RANGE, KV_ERR_DUP); KV_ERR_OOM when no block is free.  On an error nothing has changed.
+ * Host only. */
+KV_API int kv_pool_fork_blocks(kv_pool *pool, int64_t n_tokens, const int32_t *ids, int32_t *child_ids,
+                               kv_page_copy *tail);
+
+/* Plans a compaction: pairs the highest allocated blocks with the lowest free ones, while
+ * the first lie above the second, up to max_moves (0 .. KV_MAX_PAGE_COPIES) of them.  Writes
+ * the moves, whole pages, src ascending, and their number.  The allocator then holds the dst
+ * blocks with the src blocks' references, and each src block still, with one reference of
+ * its own: the caller copies the pages (kv_copy_pages), rewrites the block tables on the
+ * device (kv_remap_tables) and in its own memory, and, once nothing reads the old pages, frees the
+ * src ids.  Host only. */
+KV_API int kv_pool_plan_compact(kv_pool *pool, int32_t max_moves, kv_page_copy *moves, int32_t *n_moves);
 
 /* ---- calls -------------------------------------------------------------------- */
 
@@ -353,6 +448,76 @@ KV_API int kv_gather_chunks_dma(kv_pool *pool, const kv_span *spans, int32_t n_s
 KV_API int kv_scatter_chunks_dma(kv_pool *pool, const kv_span *spans, int32_t n_spans,
                                  const kv_chunk_spec *spec, hipStream_t stream);
 
+/* ---- pages within a pool --------------------------------------------------------- */
+
+/* Copies pages within the pool: for every record, layer in [layer_begin, layer_end) and kv,
+ * tokens [0, n_tokens) of block src to the same tokens of block dst; the rest of dst is left
+ * as it was.  One kernel launch on `stream`.  copies is a host array of n (0 ..
+ * KV_MAX_PAGE_COPIES) records.  Ids lie in [0, num_blocks) (KV_ERR_RANGE); no dst is named
+ * twice or is the src of a record (KV_ERR_DUP): every byte has one writer and no byte that
+ * is read is written.  Allocated or not is not looked at.  n == 0 is a no-op.  Returns after enqueueing.  Under
+ * graph capture a call of at most 128 records is captured as its kernel once the pool has made a
+ * call outside the capture; any other is refused with KV_ERR_CAPTURE.
+ * No passage: the page maintenance next to the pages' transfers. */
+KV_API int kv_copy_pages(kv_pool *pool, const kv_page_copy *copies, int32_t n, int32_t layer_begin,
+                         int32_t layer_end, hipStream_t stream);
+
+/* Rewrites `count` entries of block tables (device int32 arrays, 4-byte aligned) after
+ * moves: out[i] = dst of the move whose src is in[i], or in[i] where there is none (entries out of range
+ * included).  in == out rewrites in place; arrays that overlap otherwise are refused
+ * (KV_ERR_ARG).  moves is a host array of n records as in kv_copy_pages (n_tokens is not
+ * read), ids in range (KV_ERR_RANGE), no src twice (KV_ERR_DUP).  Asynchronous, one launch;
+ * captured like kv_copy_pages. */
+KV_API int kv_remap_tables(kv_pool *pool, const kv_page_copy *moves, int32_t n, const int32_t *in,
+                           int32_t *out, int64_t count, hipStream_t stream);
+
+/* ---- new tokens: append and attention -------------------------------------------- */
+
+/* A plan holds, on the device, one step's sequences, the split of their attention over the chip, and
+ * the workspace of partial results; it is set once a step and used by every layer.  The
+ * pool has num_kv 2, elem_bytes 1 for KV_TYPE_E4M3 and 2 else, head_dim <= KV_MAX_ATTN_DIM
+ * (else KV_ERR_ARG), and head_dim * elem_bytes a multiple of 16 (KV_ERR_ALIGN).  create
+ * allocates all device memory the plan will use, on the current device, which is then the
+ * pool's; it must not be made while a stream captures (KV_ERR_HIP).  destroy waits for the device
+ * to be idle first; NULL is accepted.  A plan is destroyed before its pool. */
+KV_API int kv_attn_plan_create(kv_pool *pool, const kv_attn_desc *desc, kv_attn_plan **out);
+KV_API int kv_attn_plan_destroy(kv_attn_plan *plan);
+
+/* Sets the plan to n (0 .. max_seqs) sequences: host work proportional to the
+ * pieces of work, and one stream-ordered upload.  Errors: KV_ERR_ARG (negative lengths, null
+ * table of a sequence with kv_len > 0, more sequences or rows than the plan holds), KV_ERR_RANGE (a table too
+ * short or past its allocation, kv_len over its limit), KV_ERR_DUP (two sequences
+ * own one row), KV_ERR_CAPTURE (the stream is capturing); the plan then stays as it was.
+ * The calls that use one plan -- set, append, attend, replays of graphs they were captured
+ * into -- share its memory: two that could overlap (different streams with no ordering
+ * between them) must not be made. */
+KV_API int kv_attn_plan_set(kv_attn_plan *plan, const kv_seq *seqs, int32_t n, hipStream_t stream);
+
+/* Writes the new tokens' k and v rows into their pages of one layer: the token at position
+ * p goes to slot p % block_size of block block_table[p / block_size].  An e4m3 pool gets x / scale, rounded to
+ * nearest even and saturated at +-448; NaN stays NaN.  Rows of no sequence are not read.  KV_ERR_ARG when a
+ * sequence has q_len > kv_len.  Two sequences must not write one pool token.  A block id out of
+ * range is skipped and reported (kv_pool_get_error).
+ * Append and attend make their launches and nothing else, so both can be captured into a
+ * graph; a replay works on what the last kv_attn_plan_set on its stream set, within the arrays
+ * the captured call named (rows past its n_tokens are neither read nor written). */
+KV_API int kv_append_tokens(kv_attn_plan *plan, int32_t layer, const kv_append_args *args, hipStream_t stream);
+
+/* Attention of the new tokens over the cache of one layer.  With p = kv_len - q_len + i the
+ * position of a query, it sees cached token j < kv_len where KV_ATTN_FULL is set, or j <
+ * prefix_len, or j <= p and (window == 0 or j > p - window).  Scores are s = scale * k_scale *
+ * <q, k_j>, then softcap * tanh(s / softcap) if softcap > 0, then s - slope * |p - j| if
+ * slopes are given; out = v_scale * sum_j softmax(s)_j v_j, lse = log sum_j exp(s_j) (natural).
+ * A query that sees nothing gets out = 0 and lse = -infinity.  Cached tokens that a query
+ * does not see do not reach its result, whatever they hold (infinities and NaN too); pages
+ * that no query sees are not read and their table entries may be anything.  Sums, maxima and
+ * products are held in 32 bits; the weights are rounded to q_type for the second product.  Rows of no sequence are left as they
+ * were.  The result does not depend on the run: no atomics take part.  The new tokens must
+ * be in the cache already (kv_append_tokens on the same stream).  A block id out of range
+ * is reported (kv_pool_get_error) and block 0 read in its place: the result of the queries that see it is
+ * undefined.  Captured, a call holds the kernels for any sequences within the plan's limits. */
+KV_API int kv_attend(kv_attn_plan *plan, int32_t layer, const kv_attend_args *args, hipStream_t stream);
+
 /* Synchronizes `stream`, then reads and clears the pool's sticky device error
  * word.  *out_bits receives KV_DEVERR_* bits (0 if none); the return value is
  * KV_ERR_DEVICE when any bit was set, else KV_OK.
@@ -413,7 +578,7 @@ KV_API const char *kv_strerror(int code);
 
 /* Library version: major*10000 + minor*100 + patch (KV_VERSION of the header the
  * library was built with).  No passage: library infrastructure. */
-#define KV_VERSION 200
+#define KV_VERSION 300
 KV_API int kv_version(void);
 
 /* The hipError_t of the last HIP runtime call that failed inside the library on

@@ -35,7 +35,14 @@ KV_DEVERR_BLOCK_RANGE = 0x1
 KV_RING_COHERENT = 0x0
 KV_RING_NONCOHERENT = 0x1
 KV_MAX_SPANS = 4096
-KV_VERSION = 200
+KV_MAX_PAGE_COPIES = 65536
+KV_MAX_SEQS = 4096
+KV_MAX_ATTN_DIM = 256
+KV_TYPE_F16 = 0
+KV_TYPE_BF16 = 1
+KV_TYPE_E4M3 = 2
+KV_ATTN_FULL = 0x1
+KV_VERSION = 300
 
 
 class kv_pool_desc(ctypes.Structure):
@@ -64,6 +71,38 @@ class kv_chunk_spec(ctypes.Structure):
 class kv_transfer_info(ctypes.Structure):
     _fields_ = [("tiles", ctypes.c_int64), ("chunks", ctypes.c_int64),
                 ("payload_bytes", ctypes.c_int64), ("max_chunk_bytes", ctypes.c_int64)]
+
+
+class kv_page_copy(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_int32), ("dst", ctypes.c_int32), ("n_tokens", ctypes.c_int32)]
+
+
+class kv_seq(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("table_len", ctypes.c_int64),
+                ("kv_len", ctypes.c_int64), ("q_begin", ctypes.c_int64),
+                ("q_len", ctypes.c_int32), ("prefix_len", ctypes.c_int32)]
+
+
+class kv_attn_desc(ctypes.Structure):
+    _fields_ = [("num_q_heads", ctypes.c_int32), ("q_type", ctypes.c_int32), ("kv_type", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("flags", ctypes.c_int32), ("max_seqs", ctypes.c_int32),
+                ("max_tokens", ctypes.c_int64)]
+
+
+class kv_append_args(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_token_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+                ("v_token_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+                ("n_tokens", ctypes.c_int64), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
+class kv_attend_args(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("alibi_slopes", ctypes.c_void_p),
+                ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("out_token_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+                ("n_tokens", ctypes.c_int64), ("scale", ctypes.c_float), ("softcap", ctypes.c_float),
+                ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
 
 
 def _addr(x) -> int:
@@ -103,6 +142,57 @@ def make_chunk_spec(layout: int, chunk_layers: int, chunk_tokens: int, layer_beg
                     max_workgroups: int = 0, flags: int = 0) -> kv_chunk_spec:
     return kv_chunk_spec(layout, chunk_layers, chunk_tokens, layer_begin, layer_end, _addr(base),
                          slot_bytes, n_slots, max_workgroups, flags)
+
+
+def make_page_copies(copies: Iterable) -> ctypes.Array:
+    """copies: (src, dst, n_tokens) triples, also for the moves of kv_remap_tables."""
+    copies = list(copies)
+    arr = (kv_page_copy * max(1, len(copies)))()
+    for i, (src, dst, n) in enumerate(copies):
+        arr[i] = kv_page_copy(int(src), int(dst), int(n))
+    arr._n = len(copies)
+    return arr
+
+
+def make_seqs(seqs: Iterable) -> ctypes.Array:
+    """seqs: (block_table, table_len, kv_len, q_begin, q_len[, prefix_len]) tuples; block_table is a device
+    address or tensor."""
+    seqs = list(seqs)
+    arr = (kv_seq * max(1, len(seqs)))()
+    for i, (tbl, n, kv_len, q_begin, q_len, *prefix) in enumerate(seqs):
+        arr[i] = kv_seq(_addr(tbl), int(n), int(kv_len), int(q_begin), int(q_len), int(prefix[0]) if prefix else 0)
+    arr._n = len(seqs)
+    return arr
+
+
+def make_attn_desc(num_q_heads: int, q_type: int, kv_type: int, max_seqs: int, max_tokens: int,
+                   window: int = 0, flags: int = 0) -> kv_attn_desc:
+    return kv_attn_desc(num_q_heads, q_type, kv_type, window, flags, max_seqs, max_tokens)
+
+
+def _strides(x, strides):
+    """(token, head) strides in elements: those given, or those of a [tokens][heads][dim] tensor,
+    whose innermost dimension must be packed."""
+    if strides is not None:
+        return int(strides[0]), int(strides[1])
+    if x.dim() != 3 or (x.shape[2] > 1 and x.stride(2) != 1):
+        raise ValueError("a [tokens][heads][dim] tensor with packed dim, or its address and strides")
+    return x.stride(0), x.stride(1)
+
+
+def make_append_args(k, v, n_tokens: int, k_scale: float = 1.0, v_scale: float = 1.0, k_strides=None,
+                     v_strides=None) -> kv_append_args:
+    """k and v: [n_tokens][heads][dim] tensors, or device addresses with their (token, head) strides."""
+    return kv_append_args(_addr(k), _addr(v), *_strides(k, k_strides), *_strides(v, v_strides), n_tokens, k_scale,
+                          v_scale)
+
+
+def make_attend_args(q, out, lse=None, *, n_tokens: int, scale: float, softcap: float = 0.0, alibi_slopes=None,
+                     k_scale: float = 1.0, v_scale: float = 1.0, q_strides=None, out_strides=None) -> kv_attend_args:
+    """q and out: [n_tokens][query heads][dim] tensors, or device addresses with their (token, head)
+    strides; lse: [n_tokens][query heads] float32 or None."""
+    return kv_attend_args(_addr(q), _addr(out), _addr(lse), _addr(alibi_slopes), *_strides(q, q_strides),
+                          *_strides(out, out_strides), n_tokens, scale, softcap, k_scale, v_scale)
 
 
 def _nspans(spans) -> int:

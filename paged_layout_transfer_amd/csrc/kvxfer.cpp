@@ -21,11 +21,15 @@
 
 #include "kvxfer_host.h"
 #include "kvxfer_internal.h"
+#include "kvxfer_pool.h"
 
 namespace {
 
+using kvx::SlotRange;
+using kvx::SpanPlan;
+using kvx::kInflight;
+
 constexpr int64_t kArenaBytes = 4 << 20; // span records of the calls in flight, per pool
-constexpr int kInflight = 256;           // calls in flight per pool before the host waits
 constexpr int kMaxTimed = 4096;         // launches one timing window can record
 constexpr int64_t kMaxU31 = 0x7fffffffLL;
 
@@ -35,7 +39,9 @@ constexpr int64_t kMaxU31 = 0x7fffffffLL;
 thread_local int g_hip_error = 0;
 thread_local const char *g_hip_where = "";
 
-inline bool hip_ok(hipError_t e, const char *where)
+}  // namespace
+
+bool kvx::hip_ok(hipError_t e, const char *where)
 {
     if (e == hipSuccess) return true;
     g_hip_error = (int)e;
@@ -43,20 +49,14 @@ inline bool hip_ok(hipError_t e, const char *where)
     (void)hipGetLastError();
     return false;
 }
-#define HIP_OK(call) hip_ok((call), #call)
+#define HIP_OK(call) kvx::hip_ok((call), #call)
+
+namespace {
+
+using kvx::hip_ok;
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-struct SlotRange {
-    int64_t start;  // first slot
-    int64_t count;  // chunks
-};
-
-// Per-span figures of a validated call.
-struct SpanPlan {
-    int64_t n_pages, ppc, n_tc, n_chunks, tiles;
-};
 
 int check_desc(const kv_pool_desc *d)
 {
@@ -293,41 +293,6 @@ int prepare_call(const kv_pool_desc *d, const kv_span *spans, int32_t n_spans,
 
 }  // namespace kvx
 
-struct kv_pool {
-    kv_pool_desc desc;
-    std::vector<void *> bases;
-    // allocator: free-block bitmap, lowest ids first
-    kvx::BlockBitmap blocks;
-    // validation scratch (no allocation on the call path)
-    std::vector<SpanPlan> plans;
-    std::vector<SlotRange> ranges;
-    // host image of the static device scratch (kv_transfer_chunks_noalloc), made at create
-    std::vector<uint64_t> scr_image;
-    // device state, created on the first transfer
-    int device = -1;
-    uint8_t **d_regions = nullptr;
-    int32_t *d_err = nullptr;
-    // Span-record arena: each call takes the next free stretch of a circular buffer
-    // (pinned host mirror + device copy) and records an event after its kernel; a
-    // stretch is reused once that event has passed.  Allocation is sequential, so
-    // the oldest call in flight is always the next one in the way.
-    uint8_t *d_arena = nullptr;
-    uint8_t *h_arena = nullptr;
-    kvx::ArenaRing<kInflight> arena;
-    hipEvent_t fl_ev[kInflight] = {};  // one per arena slot
-    // staging-memory kind of the last staging base seen
-    kvx::StagingKind staging_kind;
-    // the declared extents of the regions, staging bases and block tables against
-    // the allocations holding them (see check_buffers); the regions are checked until
-    // they have passed once
-    kvx::ExtentCache extents;
-    bool regions_ok = false;
-    // timing
-    bool timing = false;
-    int n_timed = 0;
-    std::vector<hipEvent_t> t_ev;
-};
-
 struct kv_ring {
     void *host = nullptr;
     void *dev = nullptr;
@@ -355,6 +320,10 @@ void free_device_state(kv_pool *p)
     if (p->d_regions) (void)hipFree(p->d_regions), p->d_regions = nullptr;
     p->device = -1;
 }
+
+}  // namespace
+
+namespace kvx {
 
 // Reserve `bytes` of the span-record arena for one call, waiting for the calls
 // that still use them (or for the oldest call when kInflight are queued).
@@ -401,6 +370,14 @@ fail:
     free_device_state(p);
     return KV_ERR_HIP;
 }
+
+}  // namespace kvx
+
+namespace {
+
+using kvx::arena_commit;
+using kvx::arena_take;
+using kvx::device_setup;
 
 void device_teardown(kv_pool *p)
 {
@@ -475,10 +452,31 @@ kvx::AllocRange alloc_range(uintptr_t q)
     return kvx::AllocRange{b, b + size};
 }
 
-int check_extent(kvx::ExtentCache &c, const void *q, int64_t bytes, kvx::AllocRange *here = nullptr)
+}  // namespace
+
+namespace kvx {
+
+int check_extent(ExtentCache &c, const void *q, int64_t bytes, AllocRange *here)
 {
     return c.covers(q, bytes, alloc_range, here) ? KV_OK : KV_ERR_RANGE;
 }
+
+int check_regions(kv_pool *p)
+{
+    if (p->regions_ok) return KV_OK;
+    const kv_pool_desc &d = p->desc;
+    const int64_t extent = (int64_t)(d.num_blocks - 1) * d.block_stride + tok_bytes(&d) * d.block_size;
+    for (void *b : p->bases)
+        if (check_extent(p->extents, b, extent)) return KV_ERR_RANGE;
+    p->regions_ok = true;
+    return KV_OK;
+}
+
+}  // namespace kvx
+
+namespace {
+
+using kvx::check_extent;
 
 // Extents of a validated call: every region (until they have passed once), the
 // staging area, and, when the tables are device memory, each span's block table.
@@ -486,13 +484,7 @@ int check_extent(kvx::ExtentCache &c, const void *q, int64_t bytes, kvx::AllocRa
 int check_buffers(kv_pool *p, const kv_span *spans, int32_t n_spans, const kv_chunk_spec *spec,
                   bool device_tables, kvx::AllocRange *staging = nullptr)
 {
-    const kv_pool_desc &d = p->desc;
-    if (!p->regions_ok) {
-        const int64_t extent = (int64_t)(d.num_blocks - 1) * d.block_stride + tok_bytes(&d) * d.block_size;
-        for (void *b : p->bases)
-            if (check_extent(p->extents, b, extent)) return KV_ERR_RANGE;
-        p->regions_ok = true;
-    }
+    if (kvx::check_regions(p)) return KV_ERR_RANGE;
     if (check_extent(p->extents, spec->base, spec->n_slots * spec->slot_bytes, staging)) return KV_ERR_RANGE;
     if (device_tables) {
         // spans often share one table: a table no longer than the last one checked at

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <unordered_map>
 #include <vector>
 
 #include "kvxfer_internal.h"
@@ -144,6 +145,7 @@ struct BlockBitmap {
         return KV_OK;
     }
 
+    // A block with more than one reference loses one; the others become free.
     int release(int32_t n, const int32_t *ids)
     {
         for (int32_t i = 0; i < n; ++i) {
@@ -154,9 +156,84 @@ struct BlockBitmap {
             }
             free_bits[(size_t)(id >> 6)] |= 1ull << (id & 63);
         }
-        for (int32_t i = 0; i < n; ++i) low_word = std::min<int64_t>(low_word, ids[i] >> 6);
-        n_free += n;
+        for (int32_t i = 0; i < n; ++i) {
+            if (!extra.empty()) {
+                const auto e = extra.find(ids[i]);
+                if (e != extra.end()) {
+                    if (--e->second == 0) extra.erase(e);
+                    free_bits[(size_t)(ids[i] >> 6)] &= ~(1ull << (ids[i] & 63));
+                    continue;
+                }
+            }
+            low_word = std::min<int64_t>(low_word, ids[i] >> 6);
+            ++n_free;
+        }
         return KV_OK;
+    }
+
+    // References of an allocated block beyond its first, held only for blocks that have
+    // any.  Not bounded by a small type: 2^31 - 2 of them.
+    std::unordered_map<int32_t, int32_t> extra;
+
+    bool allocated(int64_t id) const { return id >= 0 && id < n_blocks && !is_free(id); }
+    int64_t refs(int32_t id) const
+    {
+        if (is_free(id)) return 0;
+        const auto e = extra.find(id);
+        return e == extra.end() ? 1 : 1 + (int64_t)e->second;
+    }
+
+    // One more reference on each id; all of them or none.
+    int share(int32_t n, const int32_t *ids)
+    {
+        for (int32_t i = 0; i < n; ++i)
+            if (!allocated(ids[i])) return KV_ERR_RANGE;
+        int32_t done = 0;
+        int rc = KV_OK;
+        try {
+            for (; done < n; ++done) {
+                int32_t &e = extra[ids[done]];
+                if (e == INT32_MAX - 1) {
+                    rc = KV_ERR_RANGE;
+                    break;
+                }
+                ++e;
+            }
+        } catch (...) {
+            rc = KV_ERR_OOM;
+        }
+        if (rc)
+            while (done > 0) {
+                const auto e = extra.find(ids[--done]);
+                if (--e->second == 0) extra.erase(e);
+            }
+        return rc;
+    }
+
+    // The moves of a compaction (kv_pool_plan_compact): the lowest free blocks take the
+    // references of the highest allocated ones, which keep one.
+    int32_t compact(int32_t max_moves, int32_t block_size, kv_page_copy *moves)
+    {
+        int64_t lo = low_word * 64, hi = n_blocks - 1;
+        int32_t n = 0;
+        for (; n < max_moves; ++n) {
+            while (lo < hi && !is_free(lo)) lo += free_bits[(size_t)(lo >> 6)] ? 1 : 64 - (lo & 63);
+            while (hi > lo && is_free(hi)) hi -= ~free_bits[(size_t)(hi >> 6)] ? 1 : 1 + (hi & 63);
+            if (lo >= hi) break;
+            moves[n] = kv_page_copy{(int32_t)hi--, (int32_t)lo++, block_size};
+        }
+        for (int32_t i = 0; i < n; ++i) {
+            const kv_page_copy &m = moves[i];
+            free_bits[(size_t)(m.dst >> 6)] &= ~(1ull << (m.dst & 63));
+            auto node = extra.extract(m.src);  // the node moves with its key: nothing is allocated
+            if (!node.empty()) {
+                node.key() = m.dst;
+                extra.insert(std::move(node));
+            }
+        }
+        n_free -= n;
+        std::reverse(moves, moves + n);
+        return n;
     }
 };
 

@@ -64,6 +64,17 @@ _sig("kv_transfer_chunks_noalloc", ctypes.c_int, _P, _I32, ctypes.POINTER(kv_spa
      ctypes.POINTER(kv_chunk_spec), _P, _P)
 _sig("kv_gather_chunks_dma", ctypes.c_int, _P, ctypes.POINTER(kv_span), _I32, ctypes.POINTER(kv_chunk_spec), _P)
 _sig("kv_scatter_chunks_dma", ctypes.c_int, _P, ctypes.POINTER(kv_span), _I32, ctypes.POINTER(kv_chunk_spec), _P)
+_sig("kv_pool_share_blocks", ctypes.c_int, _P, _I32, _P)
+_sig("kv_pool_block_refs", ctypes.c_int, _P, _I32, ctypes.POINTER(_I32))
+_sig("kv_pool_fork_blocks", ctypes.c_int, _P, _I64, _P, _P, ctypes.POINTER(kv_page_copy))
+_sig("kv_pool_plan_compact", ctypes.c_int, _P, _I32, ctypes.POINTER(kv_page_copy), ctypes.POINTER(_I32))
+_sig("kv_copy_pages", ctypes.c_int, _P, ctypes.POINTER(kv_page_copy), _I32, _I32, _I32, _P)
+_sig("kv_remap_tables", ctypes.c_int, _P, ctypes.POINTER(kv_page_copy), _I32, _P, _P, _I64, _P)
+_sig("kv_attn_plan_create", ctypes.c_int, _P, ctypes.POINTER(kv_attn_desc), ctypes.POINTER(_P))
+_sig("kv_attn_plan_destroy", ctypes.c_int, _P)
+_sig("kv_attn_plan_set", ctypes.c_int, _P, ctypes.POINTER(kv_seq), _I32, _P)
+_sig("kv_append_tokens", ctypes.c_int, _P, _I32, ctypes.POINTER(kv_append_args), _P)
+_sig("kv_attend", ctypes.c_int, _P, _I32, ctypes.POINTER(kv_attend_args), _P)
 _sig("kv_pool_get_error", ctypes.c_int, _P, _P, ctypes.POINTER(_I32))
 _sig("kv_pool_timing_start", ctypes.c_int, _P)
 _sig("kv_pool_timing_read", ctypes.c_int, _P, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_I64))
@@ -83,6 +94,9 @@ EXPORTED = ("kv_pool_create", "kv_pool_destroy", "kv_pool_alloc_blocks", "kv_poo
             "kv_pool_free_count", "kv_check_transfer", "kv_chunk_bytes", "kv_validate_targets",
             "kv_gather_chunks", "kv_scatter_chunks", "kv_transfer_chunks_noalloc",
             "kv_gather_chunks_dma", "kv_scatter_chunks_dma",
+            "kv_pool_share_blocks", "kv_pool_block_refs", "kv_pool_fork_blocks", "kv_pool_plan_compact",
+            "kv_copy_pages", "kv_remap_tables", "kv_attn_plan_create", "kv_attn_plan_destroy", "kv_attn_plan_set",
+            "kv_append_tokens", "kv_attend",
             "kv_pool_get_error", "kv_pool_timing_start",
             "kv_pool_timing_read", "kv_pool_timing_read_each", "kv_ring_create", "kv_ring_slot", "kv_ring_destroy",
             "kv_ring_record", "kv_ring_wait", "kv_ring_stream_wait",
@@ -195,6 +209,67 @@ def kv_scatter_chunks_dma(pool: int, spans, spec: kv_chunk_spec, stream=None) ->
     with KV_FLAG_DMA_STRIDED); the spans' block tables are host arrays."""
     _check(_lib.kv_scatter_chunks_dma(pool, spans, _nspans(spans), ctypes.byref(spec), _stream(stream)),
            "kv_scatter_chunks_dma")
+
+
+def kv_pool_share_blocks(pool: int, ids) -> None:
+    ids = np.ascontiguousarray(ids, dtype=np.int32)
+    _check(_lib.kv_pool_share_blocks(pool, ids.size, ids.ctypes.data), "kv_pool_share_blocks")
+
+
+def kv_pool_block_refs(pool: int, block: int) -> int:
+    n = ctypes.c_int32()
+    _check(_lib.kv_pool_block_refs(pool, block, ctypes.byref(n)), "kv_pool_block_refs")
+    return n.value
+
+
+def kv_pool_fork_blocks(pool: int, n_tokens: int, ids) -> tuple[np.ndarray, tuple[int, int, int] | None]:
+    """The child's block ids, and the (src, dst, n_tokens) copy that fills its last page or
+    None; ids holds the parent's blocks, one per page of n_tokens."""
+    ids = np.ascontiguousarray(ids, dtype=np.int32)
+    child, tail = ids.copy(), kv_page_copy()
+    _check(_lib.kv_pool_fork_blocks(pool, n_tokens, ids.ctypes.data, child.ctypes.data, ctypes.byref(tail)),
+           "kv_pool_fork_blocks")
+    return child, (tail.src, tail.dst, tail.n_tokens) if tail.n_tokens else None
+
+
+def kv_pool_plan_compact(pool: int, max_moves: int) -> ctypes.Array:
+    """The moves of a compaction, as make_page_copies builds them."""
+    moves, n = (kv_page_copy * max(1, max_moves))(), ctypes.c_int32()
+    _check(_lib.kv_pool_plan_compact(pool, max_moves, moves, ctypes.byref(n)), "kv_pool_plan_compact")
+    moves._n = n.value
+    return moves
+
+
+def kv_copy_pages(pool: int, copies, layer_begin: int, layer_end: int, stream=None) -> None:
+    _check(_lib.kv_copy_pages(pool, copies, _nspans(copies), layer_begin, layer_end, _stream(stream)),
+           "kv_copy_pages")
+
+
+def kv_remap_tables(pool: int, moves, tables, out, count: int, stream=None) -> None:
+    _check(_lib.kv_remap_tables(pool, moves, _nspans(moves), _addr(tables), _addr(out), count, _stream(stream)),
+           "kv_remap_tables")
+
+
+def kv_attn_plan_create(pool: int, desc: kv_attn_desc) -> int:
+    h = ctypes.c_void_p()
+    _check(_lib.kv_attn_plan_create(pool, ctypes.byref(desc), ctypes.byref(h)), "kv_attn_plan_create")
+    return h.value
+
+
+def kv_attn_plan_destroy(plan: int) -> None:
+    _check(_lib.kv_attn_plan_destroy(plan), "kv_attn_plan_destroy")
+
+
+def kv_attn_plan_set(plan: int, seqs, stream=None) -> None:
+    _check(_lib.kv_attn_plan_set(plan, seqs, _nspans(seqs), _stream(stream)), "kv_attn_plan_set")
+
+
+def kv_append_tokens(plan: int, layer: int, args: kv_append_args, stream=None) -> None:
+    _check(_lib.kv_append_tokens(plan, layer, ctypes.byref(args), _stream(stream)), "kv_append_tokens")
+
+
+def kv_attend(plan: int, layer: int, args: kv_attend_args, stream=None) -> None:
+    _check(_lib.kv_attend(plan, layer, ctypes.byref(args), _stream(stream)), "kv_attend")
 
 
 def kv_pool_get_error(pool: int, stream=None) -> int:
