@@ -18,6 +18,8 @@
 #pragma once
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "kvxfer_ops.h"
 
 namespace kvx {
@@ -70,26 +72,56 @@ __device__ __forceinline__ typename Vec<T>::x4 from_e4m3(uint32_t w)
     return typename Vec<T>::x4{a[0], a[1], b[0], b[1]};
 }
 
-// Whether any of eight 16-bit values is an infinity or a NaN.
+// The infinities and NaN among eight 16-bit values, one truth value each.
 template <class T>
-__device__ __forceinline__ bool not_finite(typename Vec<T>::x8 v)
+__device__ __forceinline__ bool not_finite(uint16_t x)
+{
+    constexpr uint16_t e = __is_same(T, __bf16) ? 0x7f80u : 0x7c00u;
+    return (x & e) == e;
+}
+template <class T>
+__device__ __forceinline__ bool any_not_finite(typename Vec<T>::x8 v)
 {
     constexpr uint32_t e = __is_same(T, __bf16) ? 0x7f80u : 0x7c00u;
     const u32x4 w = __builtin_bit_cast(u32x4, v);
     bool bad = false;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) bad |= (w[i] & e) == e || (w[i] & (e << 16)) == (e << 16);
+    for (int i = 0; i < 4; ++i) bad |= ((w[i] & e) == e) | ((w[i] & (e << 16)) == (e << 16));
     return bad;
 }
-
-// 16-bit storage of one tile in shared memory: rows of DP values in 16-byte chunks, chunk c
-// of row r at c ^ (r mod chunks), so that reads down a column meet different banks.
-template <int DP>
-__device__ __forceinline__ int lds_at(int row, int chunk)
+typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+// The values with zeros for infinities and NaN.
+template <class T>
+__device__ __forceinline__ typename Vec<T>::x8 only_finite(typename Vec<T>::x8 v)
 {
-    constexpr int C = DP / 8, M = C < 16 ? C : 16;
-    return row * DP + ((chunk ^ (row & (M - 1))) << 3);
+    u16x8 w = __builtin_bit_cast(u16x8, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = not_finite<T>(w[i]) ? 0 : w[i];
+    return __builtin_bit_cast(typename Vec<T>::x8, w);
 }
+// Ones where the values are of one kind: 0 NaN, 1 +infinity, 2 -infinity.
+template <class T>
+__device__ __forceinline__ typename Vec<T>::x8 ones_at(typename Vec<T>::x8 v, int kind)
+{
+    constexpr uint16_t inf = __is_same(T, __bf16) ? 0x7f80u : 0x7c00u, one = __is_same(T, __bf16) ? 0x3f80u : 0x3c00u;
+    u16x8 w = __builtin_bit_cast(u16x8, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const bool is = kind == 0 ? (w[i] & 0x7fff) > inf : w[i] == (kind == 1 ? inf : inf | 0x8000u);
+        w[i] = is ? one : 0;
+    }
+    return __builtin_bit_cast(typename Vec<T>::x8, w);
+}
+__device__ __forceinline__ float special(int kind) { return kind == 0 ? __builtin_nanf("") : kind == 1 ? INFINITY : -INFINITY; }
+
+// Rows of a tile in shared memory, in values.  Key rows are one 16-byte chunk longer than
+// their values, so that the 16 lanes that read one chunk of 16 rows meet all banks; value rows 64
+// bytes, so that the transposing reads' 64-byte stretches of four rows do.  (Exchanging chunks
+// instead saves the space, but takes an address register for each chunk.)
+template <int DP>
+constexpr int key_row() { return DP + 8; }
+template <int DP>
+constexpr int value_row() { return DP + 32; }
 
 // Four consecutive rows of one column, transposed: the 16 lanes of a group read 4 rows of
 // 16 values, lane i giving the address of values 4 (i mod 4) .. +3 of row i / 4, and lane i
@@ -151,10 +183,12 @@ __device__ __forceinline__ RowMask row_mask(const AttnLaunch &a, const Piece &s,
     return m;
 }
 
-// Whether any row of the piece sees key j.
-__device__ __forceinline__ bool any_sees(const Piece &s, int32_t j)
+// The key to read in j's place: j itself if some row sees it, else a neighbour that some row
+// sees, so that no page is read, and no table entry followed, that nothing sees.
+__device__ __forceinline__ int32_t seen_key(const Piece &s, int32_t j)
 {
-    return j < s.walk.prefix || (j >= s.walk.low && j < s.walk.high);
+    const int32_t k = min(max(j, s.walk.low), s.walk.high - 1);
+    return j < s.walk.prefix ? j : s.walk.high > s.walk.low ? k : s.walk.prefix - 1;
 }
 
 // Whether every row of the piece sees the n keys from j on: the scores need no mask.
@@ -165,19 +199,20 @@ __device__ __forceinline__ bool all_see(const AttnLaunch &a, const Piece &s, int
     return j + n - 1 <= s.p0 && (a.window == 0 || j > s.p1 - a.window);
 }
 
-// Byte offset in a region of key j's row (of the piece's head).  A key that no row sees is
-// not looked up: offset -1.  A block id out of range is reported, and block 0 read.
-__device__ __forceinline__ int64_t key_offset(const AttnLaunch &a, const Piece &s, int32_t j)
+// The block that holds key j, and where key j's row (of the piece's head) starts in a region.  A
+// block id out of range is reported, and block 0 read.
+__device__ __forceinline__ int32_t block_of(const AttnLaunch &a, const Piece &s, int32_t j)
 {
-    if (!any_sees(s, j)) return -1;
-    const uint32_t page = div_by((uint32_t)j, a.bs_magic, a.bs_shift);
-    int32_t blk = s.table[page];
+    return s.table[div_by((uint32_t)j, a.bs_magic, a.bs_shift)];
+}
+__device__ __forceinline__ int64_t key_offset(const AttnLaunch &a, const Piece &s, int32_t j, int32_t blk)
+{
+    const uint32_t slot = (uint32_t)j - div_by((uint32_t)j, a.bs_magic, a.bs_shift) * a.block_size;
     if ((uint32_t)blk >= a.num_blocks) {
         atomicOr(a.err, KV_DEVERR_BLOCK_RANGE);
         blk = 0;
     }
-    return (int64_t)blk * a.block_stride + (int64_t)((uint32_t)j - page * a.block_size) * a.tok_stride +
-           (int64_t)s.head * a.head_stride;
+    return (int64_t)blk * a.block_stride + ((int64_t)slot * a.tok_stride + (int64_t)s.head * a.head_stride);
 }
 
 // Score transforms other than one positive scale: the tanh cap, the distance slopes, and
@@ -203,6 +238,7 @@ __device__ __forceinline__ void shape(const AttnLaunch &a, X &x, float slope_log
 template <int N, class X, class Key>
 __device__ __forceinline__ void hide(X &x, const RowMask &mask, Key key)
 {
+    asm volatile("");  // a tile that all rows see whole branches past the compares
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = mask.sees(key(i)) ? x[i] : -INFINITY;
 }
@@ -250,25 +286,28 @@ __device__ __forceinline__ void store_lse(const AttnLaunch &a, int64_t row, int3
 // At most 16 rows (16x16x32 products).  Four waves take the piece's 32-key steps in turn,
 // each with its own running maximum, and join at the end in shared memory.  Bound by the
 // cache's bytes: keys go from memory to the first product's registers directly, values through a
-// slice of shared memory of the wave's own, both loaded a step ahead, with no barrier in the
-// loop.
+// slice of shared memory of the wave's own, both loaded a step ahead and their block ids two, with
+// no barrier in the loop.
 template <class T, bool E4M3, int DP, bool SHAPED>
 __global__ __launch_bounds__(256) void attend_few(const AttnLaunch a)
 {
     typedef typename Vec<T>::x8 T8;
     typedef typename Vec<T>::x4 T4;
-    constexpr int kStep = 32;                  // keys of one wave's step
-    constexpr int kS = DP / 32;                // contraction steps of the first product
+    constexpr int kStep = 32;                         // keys of one wave's step
+    constexpr int kS = DP / 32;                       // contraction steps of the first product
     constexpr int kLoads = E4M3 ? DP / 64 : DP / 32;  // 16-byte loads of a lane for one key row
-    constexpr int kVals = E4M3 ? 16 : 8;       // values of one load
-    __shared__ __attribute__((aligned(16))) char shared[4 * kStep * DP * 2];
+    constexpr int kVals = E4M3 ? 16 : 8;              // values of one load
+    constexpr int kRow = value_row<DP>();
+    // each wave's values, then its 16 rows of 32-bit results
+    constexpr int kSlice = kStep * kRow * 2 > 16 * DP * 4 ? kStep * kRow * 2 : 16 * DP * 4;
+    __shared__ __attribute__((aligned(16))) char shared[4 * kSlice];
     __shared__ float join_m[4][16], join_l[4][16];
 
     if ((int32_t)blockIdx.x >= a.head->n_few) return;
     const Piece s = load_piece<16>(a);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int n = lane & 15, g = lane >> 4;
-    T *tile = (T *)(shared + wave * kStep * DP * 2);
+    T *tile = (T *)(shared + wave * kSlice);
 
     // The lane's row, and its query as the first product's right operand.  Lane group g
     // holds, for contraction step c, columns 32 c + 8 g (16-bit pools) or, so that one
@@ -279,6 +318,37 @@ __global__ __launch_bounds__(256) void attend_few(const AttnLaunch a)
     const RowMask mask = row_mask(a, s, pos);
     float slope = 0.f;
     if (SHAPED && a.slopes) slope = a.slopes[s.head * a.group + (int32_t)R - tok * a.group] * 1.4426950408889634f;
+
+    u32x4 kr[2][kLoads], vr[2][kLoads];
+    const int32_t i1 = s.tile1 * 2;
+    int32_t i = s.tile0 * 2 + wave;
+    auto start = [&](int32_t i) { return s.walk.start(i >> 1) + (i & 1) * kStep; };
+    auto key = [&](int32_t i, int t) { return seen_key(s, start(i) + 16 * t + n); };
+    auto load = [&](u32x4(&r)[2][kLoads], const uint8_t *base, const int64_t(&off)[2]) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int c = 0; c < kLoads; ++c) {
+                r[t][c] = u32x4{0, 0, 0, 0};
+                if (DP == 128 && a.dim == DP) r[t][c] = *(const KVX_GLOBAL u32x4 *)(base + off[t] + c * 64 + g * 16);
+                else if (c * 4 * kVals + g * kVals < a.dim)
+                    r[t][c] = *(const KVX_GLOBAL u32x4 *)(base + off[t] + c * 64 + g * 16);
+            }
+    };
+    int64_t off[2] = {0, 0};
+    int32_t blk[2] = {0, 0};
+    if (i < i1) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) blk[t] = block_of(a, s, key(i, t));
+#pragma unroll
+        for (int t = 0; t < 2; ++t) off[t] = key_offset(a, s, key(i, t), blk[t]);
+        load(kr, a.k_base, off);
+        load(vr, a.v_base, off);
+    }
+    if (i + 4 < i1) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) blk[t] = block_of(a, s, key(i + 4, t));
+    }
     T8 q[kS];
     const T *qr = q_row<T>(a, s, n);
 #pragma unroll
@@ -286,39 +356,17 @@ __global__ __launch_bounds__(256) void attend_few(const AttnLaunch a)
 
     f32x4 o[DP / 16];
 #pragma unroll
-    for (int i = 0; i < DP / 16; ++i) o[i] = f32x4{0, 0, 0, 0};
+    for (int d = 0; d < DP / 16; ++d) o[d] = f32x4{0, 0, 0, 0};
     float m = -INFINITY, l = 0.f;
     const float sc = SHAPED ? 1.f : a.scale_log2;
     const float slack = 8.f / sc;  // a maximum that grows by less than 2^8 is not worth a rescaling
 
-    u32x4 kr[2][kLoads], vr[2][kLoads];
-    const int32_t i1 = s.tile1 * 2;
-    int32_t i = s.tile0 * 2 + wave;
-    auto start = [&](int32_t i) { return s.walk.start(i >> 1) + (i & 1) * kStep; };
-    auto load = [&](u32x4(&r)[2][kLoads], const uint8_t *base, const int64_t(&off)[2]) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int c = 0; c < kLoads; ++c) {
-                const int d = c * 4 * kVals + g * kVals;
-                r[t][c] = u32x4{0, 0, 0, 0};
-                if (off[t] >= 0 && d < a.dim) r[t][c] = *(const KVX_GLOBAL u32x4 *)(base + off[t] + c * 64 + g * 16);
-            }
-    };
-    int64_t off[2] = {-1, -1};
-    if (i < i1) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) off[t] = key_offset(a, s, start(i) + 16 * t + n);
-        load(kr, a.k_base, off);
-        load(vr, a.v_base, off);
-    }
     for (; i < i1; i += 4) {
         const int32_t j0 = start(i);
         const bool more = i + 4 < i1;
-        int64_t next[2] = {-1, -1};
         if (more) {
 #pragma unroll
-            for (int t = 0; t < 2; ++t) next[t] = key_offset(a, s, start(i + 4) + 16 * t + n);
+            for (int t = 0; t < 2; ++t) off[t] = key_offset(a, s, key(i + 4, t), blk[t]);
         }
         // S^T: keys 16 t + 4 g + r of the step against row n
         f32x4 x[2];
@@ -337,24 +385,27 @@ __global__ __launch_bounds__(256) void attend_few(const AttnLaunch a)
                 }
             }
         }
-        if (more) load(kr, a.k_base, next);
+        if (more) load(kr, a.k_base, off);
         // V to shared memory, row-major
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int c = 0; c < kLoads; ++c) {
-                const int row = 16 * t + n;
+                T *to = tile + (16 * t + n) * kRow + c * 4 * kVals + g * kVals;
                 if constexpr (E4M3) {
                     const T4 w0 = from_e4m3<T>(vr[t][c][0]), w1 = from_e4m3<T>(vr[t][c][1]);
                     const T4 w2 = from_e4m3<T>(vr[t][c][2]), w3 = from_e4m3<T>(vr[t][c][3]);
-                    *(T8 *)(tile + lds_at<DP>(row, 8 * c + 2 * g)) = __builtin_shufflevector(w0, w1, 0, 1, 2, 3, 4, 5, 6, 7);
-                    *(T8 *)(tile + lds_at<DP>(row, 8 * c + 2 * g + 1)) =
-                        __builtin_shufflevector(w2, w3, 0, 1, 2, 3, 4, 5, 6, 7);
+                    *(T8 *)to = __builtin_shufflevector(w0, w1, 0, 1, 2, 3, 4, 5, 6, 7);
+                    *(T8 *)(to + 8) = __builtin_shufflevector(w2, w3, 0, 1, 2, 3, 4, 5, 6, 7);
                 } else {
-                    *(u32x4 *)(tile + lds_at<DP>(row, 4 * c + g)) = vr[t][c];
+                    *(u32x4 *)to = vr[t][c];
                 }
             }
-        if (more) load(vr, a.v_base, next);
+        if (more) load(vr, a.v_base, off);
+        if (i + 8 < i1) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) blk[t] = block_of(a, s, key(i + 8, t));
+        }
         // the slice is the wave's own and its accesses stay in order: no barrier, but the
         // compiler must not move the reads below above the writes of other lanes
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -362,9 +413,9 @@ __global__ __launch_bounds__(256) void attend_few(const AttnLaunch a)
         const bool masked = !all_see(a, s, j0, kStep);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            auto key = [&](int r) { return j0 + 16 * t + 4 * g + r; };
-            if (SHAPED) shape<4>(a, x[t], slope, pos, key);
-            if (masked) hide<4>(x[t], mask, key);
+            auto at = [&](int r) { return j0 + 16 * t + 4 * g + r; };
+            if (SHAPED) shape<4>(a, x[t], slope, pos, at);
+            if (masked) hide<4>(x[t], mask, at);
         }
         float mx = fmaxf(fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[0][2], x[0][3])),
                          fmaxf(fmaxf(x[1][0], x[1][1]), fmaxf(x[1][2], x[1][3])));
@@ -384,38 +435,38 @@ __global__ __launch_bounds__(256) void attend_few(const AttnLaunch a)
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const float e = __builtin_amdgcn_exp2f(x[t][r] * sc - mm);
+                const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(x[t][r], sc, -mm));
                 l += e;
                 w[4 * t + r] = (T)e;
             }
         // O^T: column d of keys 16 t + 4 g + r
-        const T *col = tile + 0;
+        const T *col = tile + (4 * g + (n >> 2)) * kRow + (n & 3) * 4;
         auto value = [&](int d) {
-            const int row = 4 * g + (n >> 2), c = 2 * d + ((n & 3) >> 1), half = (n & 1) * 4;
-            const T4 lo = read_column<T>(col + lds_at<DP>(row, c) + half);
-            const T4 hi = read_column<T>(col + lds_at<DP>(row + 16, c) + half);
+            const T4 lo = read_column<T>(col + 16 * d), hi = read_column<T>(col + 16 * kRow + 16 * d);
             return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
         };
         bool odd = false;
         if (masked) {
 #pragma unroll
-            for (int d = 0; d < DP / 16; ++d) odd |= not_finite<T>(value(d));
+            for (int d = 0; d < DP / 16; ++d) odd |= any_not_finite<T>(value(d));
         }
         if (masked && __any(odd)) {
-            // An infinity or NaN among the values: a zero weight would turn it into NaN in rows that do not
-            // see it, so the keys go one at a time and such rows leave the product out.
-            for (int key = 0; key < kStep; ++key) {
-                const int slot = (key >> 4) * 4 + (key & 3);
-                const bool here = ((key >> 2) & 3) == g, seen = mask.sees(j0 + key);
+            // An infinity or NaN among the values: a zero weight would turn it into NaN in rows
+            // that do not see it.  So it is left out of the product, and added where it is seen: where
+            // a product of ones, for seen keys and such values, is not zero.
+            T8 seen;
 #pragma unroll
-                for (int d = 0; d < DP / 16; ++d) {
-                    const T8 v = value(d);
-                    T8 vk{}, wk{};
+            for (int k = 0; k < 8; ++k)
+                seen[k] = (T)(mask.sees(j0 + 16 * (k >> 2) + 4 * g + (k & 3)) ? 1.f : 0.f);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        if (here && k == slot) vk[k] = v[k], wk[k] = w[k];
-                    const f32x4 one = mfma16(vk, wk, f32x4{0, 0, 0, 0});
-                    if (seen) o[d] += one;
+            for (int d = 0; d < DP / 16; ++d) {
+                const T8 v = value(d);
+                o[d] = mfma16(only_finite<T>(v), w, o[d]);
+#pragma unroll
+                for (int kind = 0; kind < 3; ++kind) {
+                    const f32x4 c = mfma16(ones_at<T>(v, kind), seen, f32x4{0, 0, 0, 0});
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) o[d][r] += c[r] != 0.f ? special(kind) : 0.f;
                 }
             }
         } else {
@@ -428,7 +479,7 @@ __global__ __launch_bounds__(256) void attend_few(const AttnLaunch a)
 
     // join the four waves: their slices hold 16 rows of 32-bit results
     __syncthreads();
-    float *part = (float *)shared + wave * 16 * DP;
+    float *part = (float *)tile;
     if (g == 0) join_m[wave][n] = m == -INFINITY ? m : m * sc, join_l[wave][n] = l;
     __syncthreads();
     float top = -INFINITY;
@@ -456,7 +507,7 @@ __global__ __launch_bounds__(256) void attend_few(const AttnLaunch a)
 #pragma unroll
         for (int w = 0; w < 4; ++w)
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] += ((float *)shared)[(w * 16 + row) * DP + d + k];
+            for (int k = 0; k < 8; ++k) v[k] += ((float *)(shared + w * kSlice))[row * DP + d + k];
         if (s.prow >= 0) {
             float *to = a.part_o + ((int64_t)s.prow + row) * DP + d;
             *(f32x4 *)to = f32x4{v[0], v[1], v[2], v[3]};
@@ -477,26 +528,36 @@ __global__ __launch_bounds__(256) void attend_few(const AttnLaunch a)
 
 // ---- many rows: chunks and prompts ----------------------------------------------
 
-// 128 rows, 32 a wave (32x32x16 products); the four waves share 64-key tiles of K and V in
-// shared memory, two deep, the next one loaded while the last one is worked on.
+template <int DP>
+constexpr int many_waves() { return DP == 256 ? 4 : 8; }
+
+template <int DP>
+constexpr int many_lds() { return 2 * KVX_TILE_KEYS * (key_row<DP>() + value_row<DP>()) * 2; }
+
+// 32 rows a wave (32x32x16 products); the workgroup's waves share 64-key tiles of K and V in
+// shared memory, two deep; while one is worked on, the next one is on its way to registers (and
+// the block ids of the one after it).
 template <class T, bool E4M3, int DP, bool SHAPED>
-__global__ __launch_bounds__(256) void attend_many(const AttnLaunch a)
+__global__ __launch_bounds__(64 * many_waves<DP>()) void attend_many(const AttnLaunch a)
 {
     typedef typename Vec<T>::x8 T8;
     typedef typename Vec<T>::x4 T4;
+    typedef typename Vec<T>::x2 T2;
+    constexpr int kWaves = many_waves<DP>();
     constexpr int N = KVX_TILE_KEYS;
-    constexpr int kVals = E4M3 ? 16 : 8;             // values of one 16-byte load
-    constexpr int kRow = DP / kVals;                 // loads of one key row
-    constexpr int kLoads = N * kRow / 256;           // loads of a thread for one tile
-    constexpr int kRows = 256 / kRow;                // key rows between a thread's loads
+    constexpr int kRow = DP / 8;                      // pieces of one key row: eight values each
+    constexpr int kLoads = N * kRow / (64 * kWaves);  // loads of a thread for one tile of K or V
+    static_assert(kLoads * 64 * kWaves == N * kRow, "whole loads");
     extern __shared__ __attribute__((aligned(16))) char shared[];
-    T *kt = (T *)shared, *vt = kt + 2 * N * DP;      // [2][N][DP] each
+    constexpr int kK = key_row<DP>(), kV = value_row<DP>(), kTile = N * (kK + kV);
+    T *const tiles = (T *)shared;  // [2]: K [N][kK], V [N][kV]
+    __shared__ int32_t odd[2];     // one past the last tile of this buffer with infinities or NaN in V
 
     if ((int32_t)blockIdx.x >= a.head->n_many) return;
-    const Piece s = load_piece<KVX_ROWS_MANY>(a);
+    const Piece s = load_piece<32 * kWaves>(a);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int n = lane & 31, g = lane >> 5;
-    const int rw = wave * 32 + n;  // the lane's row of the piece
+    const int rw = wave * 32 + n;              // the lane's row of the piece
 
     const uint32_t R = (uint32_t)(s.row0 + (rw < s.rows ? rw : s.rows - 1));
     const int32_t tok = (int32_t)div_by(R, a.group_magic, a.group_shift);
@@ -517,57 +578,50 @@ __global__ __launch_bounds__(256) void attend_many(const AttnLaunch a)
         for (int r = 0; r < 16; ++r) o[i][r] = 0.f;
     float m = -INFINITY, l = 0.f;
     const float sc = SHAPED ? 1.f : a.scale_log2;
-    const float slack = 8.f / sc;
+    const float slack = 8.f / sc;  // a maximum that grows by less than 2^8 is not worth a rescaling
 
-    const int lr = threadIdx.x / kRow, lc = threadIdx.x % kRow;
-    u32x4 kr[kLoads], vr[kLoads];
-    auto load = [&](int32_t i) {
-        const int32_t j0 = s.walk.start(i);
+    // The thread's pieces of a tile: eight values of key rows row0 + c * kApart.
+    typedef typename std::conditional<E4M3, u32x2, u32x4>::type Piece8;
+    constexpr int kApart = 64 * kWaves / kRow;
+    const int krow = threadIdx.x / kRow, chunk = threadIdx.x % kRow;
+    const bool inside = chunk * 8 < a.dim;  // columns past the rows' width are zeros
+    int32_t blk[kLoads];
+    Piece8 kr[kLoads], vr[kLoads];
+#pragma unroll
+    for (int c = 0; c < kLoads; ++c) kr[c] = vr[c] = Piece8{};
+    auto look_up = [&](int32_t i) __attribute__((always_inline)) {
+        const int32_t j0 = s.walk.start(i) + krow;
+#pragma unroll
+        for (int c = 0; c < kLoads; ++c) blk[c] = block_of(a, s, seen_key(s, j0 + c * kApart));
+    };
+    auto load = [&](int32_t i) __attribute__((always_inline)) {
+        const int32_t j0 = s.walk.start(i) + krow;
 #pragma unroll
         for (int c = 0; c < kLoads; ++c) {
-            const int64_t off = key_offset(a, s, j0 + lr + c * kRows);
-            kr[c] = vr[c] = u32x4{0, 0, 0, 0};
-            if (off >= 0 && lc * kVals < a.dim) {
-                kr[c] = *(const KVX_GLOBAL u32x4 *)(a.k_base + off + lc * 16);
-                vr[c] = *(const KVX_GLOBAL u32x4 *)(a.v_base + off + lc * 16);
+            const int64_t off = key_offset(a, s, seen_key(s, j0 + c * kApart), blk[c]) + chunk * (int)sizeof(Piece8);
+            if (inside) {
+                kr[c] = *(const KVX_GLOBAL Piece8 *)(a.k_base + off);
+                vr[c] = *(const KVX_GLOBAL Piece8 *)(a.v_base + off);
             }
         }
     };
-    auto put = [&](T *tile, const u32x4(&r)[kLoads]) {
-#pragma unroll
-        for (int c = 0; c < kLoads; ++c) {
-            const int row = lr + c * kRows;
-            if constexpr (E4M3) {
-                const T4 w0 = from_e4m3<T>(r[c][0]), w1 = from_e4m3<T>(r[c][1]);
-                const T4 w2 = from_e4m3<T>(r[c][2]), w3 = from_e4m3<T>(r[c][3]);
-                *(T8 *)(tile + lds_at<DP>(row, 2 * lc)) = __builtin_shufflevector(w0, w1, 0, 1, 2, 3, 4, 5, 6, 7);
-                *(T8 *)(tile + lds_at<DP>(row, 2 * lc + 1)) = __builtin_shufflevector(w2, w3, 0, 1, 2, 3, 4, 5, 6, 7);
-            } else {
-                *(u32x4 *)(tile + lds_at<DP>(row, lc)) = r[c];
-            }
-        }
+    auto widen = [&](const Piece8 &r) __attribute__((always_inline)) {
+        if constexpr (E4M3) return __builtin_shufflevector(from_e4m3<T>(r[0]), from_e4m3<T>(r[1]), 0, 1, 2, 3, 4, 5, 6, 7);
+        else return __builtin_bit_cast(T8, r);
     };
-    if (s.tile0 < s.tile1) load(s.tile0);
-    for (int32_t i = s.tile0; i < s.tile1; ++i) {
-        const int buf = (i - s.tile0) & 1;
-        T *K = kt + buf * N * DP, *V = vt + buf * N * DP;
-        put(K, kr);
-        put(V, vr);
-        __syncthreads();
-        if (i + 1 < s.tile1) load(i + 1);
 
-        const int32_t j0 = s.walk.start(i);
+    // one tile's products for the wave's rows
+    auto work = [&](const T *K, const T *V, int32_t j0, bool masked) __attribute__((always_inline)) {
         f32x16 x[2];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int r = 0; r < 16; ++r) x[t][r] = 0.f;
 #pragma unroll
-            for (int c = 0; c < DP / 16; ++c)
-                x[t] = mfma32(*(const T8 *)(K + lds_at<DP>(32 * t + n, 2 * c + g)), q[c], x[t]);
-        }
+        for (int c = 0; c < DP / 16; ++c)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) x[t] = mfma32(*(const T8 *)(K + 32 * t * kK + 16 * c), q[c], x[t]);
         // register r of tile t: key 32 t + 8 (r / 4) + 4 g + r mod 4
-        const bool masked = !all_see(a, s, j0, N);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             auto key = [&](int r) { return j0 + 32 * t + 8 * (r >> 2) + 4 * g + (r & 3); };
@@ -590,64 +644,108 @@ __global__ __launch_bounds__(256) void attend_many(const AttnLaunch a)
         }
         const float mm = m == -INFINITY ? 0.f : m * sc;
         T8 w[4];  // the weights of 16 keys each
+        float sum[2] = {0.f, 0.f};
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const float e = __builtin_amdgcn_exp2f(x[t][r] * sc - mm);
-                l += e;
-                w[2 * t + (r >> 3)][r & 7] = (T)e;
+            for (int r = 0; r < 16; r += 2) {
+                const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[t][r], sc, -mm));
+                const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[t][r + 1], sc, -mm));
+                sum[0] += e0;
+                sum[1] += e1;
+                w[2 * t + (r >> 3)][r & 7] = (T)e0;
+                w[2 * t + (r >> 3)][(r & 7) + 1] = (T)e1;
             }
+        l += sum[0] + sum[1];
         // V^T of 16 keys: slots 0-3 are keys 4 g + 0..3, slots 4-7 keys 8 + 4 g + 0..3
         auto value = [&](int d, int u) {
-            const int row = 16 * u + 4 * g + ((lane & 15) >> 2);
-            const int c = 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1), half = (lane & 1) * 4;
-            const T4 lo = read_column<T>(V + lds_at<DP>(row, c) + half);
-            const T4 hi = read_column<T>(V + lds_at<DP>(row + 8, c) + half);
+            const T4 lo = read_column<T>(V + 16 * u * kV + 32 * d), hi = read_column<T>(V + (16 * u + 8) * kV + 32 * d);
             return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
         };
-        bool odd = false;
-        if (masked) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int d = 0; d < DP / 32; ++d) o[d] = mfma32(value(d, u), w[u], o[d]);
+    };
+
+    // Infinities and NaN among the values of a tile that some rows see in part: a zero weight would
+    // turn them into NaN in rows that do not see them.  The tile's copy for the product holds
+    // zeros in their place; here each row adds those it sees, from the tile as it was (in `was`).
+    auto add_specials = [&](const T *was, int32_t j0) __attribute__((always_inline)) {
+#pragma unroll 1
+        for (int k = 0; k < N; ++k) {
+            const bool seen = mask.sees(j0 + k);
 #pragma unroll
             for (int d = 0; d < DP / 32; ++d)
 #pragma unroll
-                for (int u = 0; u < 4; ++u) odd |= not_finite<T>(value(d, u));
-        }
-        if (masked && __any(odd)) {
-            // as in attend_few: one key at a time, left out by the rows that do not see it
+                for (int r = 0; r < 4; ++r) {
+                    const T4 v = *(const T4 *)(was + k * kV + 32 * d + 8 * r + 4 * g);
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-                for (int key = 0; key < 16; ++key) {
-                    const int slot = (key >> 3) * 4 + (key & 3);
-                    const bool here = ((key >> 2) & 1) == g, seen = mask.sees(j0 + 16 * u + key);
-#pragma unroll
-                    for (int d = 0; d < DP / 32; ++d) {
-                        const T8 v = value(d, u);
-                        T8 vk{}, wk{};
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            if (here && k == slot) vk[k] = v[k], wk[k] = w[u][k];
-                        f32x16 one;
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) one[r] = 0.f;
-                        one = mfma32(vk, wk, one);
-                        if (seen) o[d] += one;
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        o[d][4 * r + e] += seen && not_finite<T>(__builtin_bit_cast(uint16_t, v[e])) ? (float)v[e] : 0.f;
                 }
-        } else {
-#pragma unroll
-            for (int d = 0; d < DP / 32; ++d)
-#pragma unroll
-                for (int u = 0; u < 4; ++u) o[d] = mfma32(value(d, u), w[u], o[d]);
         }
+    };
+
+    if (threadIdx.x < 2) odd[threadIdx.x] = 0;
+    __syncthreads();
+    if (s.tile0 < s.tile1) {
+        look_up(s.tile0);
+        load(s.tile0);
+        if (s.tile0 + 1 < s.tile1) look_up(s.tile0 + 1);
+    }
+    // Puts tile i, which has arrived, into shared memory and sends for the next one.
+    auto stage = [&](int32_t i, bool masked, auto rows) __attribute__((always_inline)) {
+        const int buf = (i - s.tile0) & 1;
+        T *K = tiles + buf * kTile, *V = K + N * kK;
+#pragma unroll
+        for (int c = 0; c < kLoads; ++c) {
+            *(T8 *)(K + (krow + c * kApart) * kK + chunk * 8) = widen(kr[c]);
+            *(T8 *)(V + (krow + c * kApart) * kV + chunk * 8) = widen(vr[c]);
+        }
+        if (masked) {
+            bool any = false;
+#pragma unroll
+            for (int c = 0; c < kLoads; ++c) any |= any_not_finite<T>(widen(vr[c]));
+            if (any) odd[buf] = i + 1;
+        }
+        __syncthreads();  // the tile is whole; and no wave still works on the other one
+        if (__builtin_expect(masked && odd[buf] == i + 1, 0)) {
+            T *was = tiles + (buf ^ 1) * kTile + N * kK;
+#pragma unroll
+            for (int c = 0; c < kLoads; ++c) {
+                const T8 v = widen(vr[c]);
+                *(T8 *)(was + (krow + c * kApart) * kV + chunk * 8) = v;
+                *(T8 *)(V + (krow + c * kApart) * kV + chunk * 8) = only_finite<T>(v);
+            }
+            __syncthreads();
+            if (decltype(rows)::value) add_specials(was, s.walk.start(i));
+            __syncthreads();  // before the next tile takes its place
+        }
+        if (i + 1 < s.tile1) load(i + 1);
+        if (i + 2 < s.tile1) look_up(i + 2);
+    };
+    auto partly = [&](int32_t i) { return !all_see(a, s, s.walk.start(i), N); };
+    if (wave * 32 >= s.rows) {  // a wave without rows only helps loading
+        for (int32_t i = s.tile0; i < s.tile1; ++i) stage(i, partly(i), std::false_type{});
+        return;
+    }
+    const int kat = n * kK + 8 * g;
+    const int vat = N * kK + (4 * g + ((lane & 15) >> 2)) * kV + ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
+    for (int32_t i = s.tile0; i < s.tile1; ++i) {
+        const bool masked = partly(i);
+        stage(i, masked, std::true_type{});
+        const T *tile = tiles + ((i - s.tile0) & 1) * kTile;
+        work(tile + kat, tile + vat, s.walk.start(i), masked);
     }
     l += __shfl_xor(l, 32);
     if (rw >= s.rows) return;
-    const int64_t row = (int64_t)s.q_begin + tok;
+    const int64_t to_row = (int64_t)s.q_begin + tok;
+    const float top = m == -INFINITY ? m : m * sc;
     if (s.prow >= 0) {
         const int64_t pr = (int64_t)s.prow + rw;
         if (g == 0) {
-            a.part_ml[2 * pr] = m == -INFINITY ? m : m * sc;
+            a.part_ml[2 * pr] = top;
             a.part_ml[2 * pr + 1] = l;
         }
 #pragma unroll
@@ -658,10 +756,10 @@ __global__ __launch_bounds__(256) void attend_many(const AttnLaunch a)
                     f32x4{o[d][4 * r], o[d][4 * r + 1], o[d][4 * r + 2], o[d][4 * r + 3]};
         return;
     }
-    if (g == 0) store_lse(a, row, head, m == -INFINITY ? m : m * sc, l);
-    if (row >= a.n_tokens) return;
+    if (g == 0) store_lse(a, to_row, head, top, l);
+    if (to_row >= a.n_tokens) return;
     const float by = l == 0.f ? 0.f : a.v_scale / l;
-    T *to = (T *)a.out + row * a.out_token + (int64_t)head * a.out_head;
+    T *to = (T *)a.out + to_row * a.out_token + (int64_t)head * a.out_head;
 #pragma unroll
     for (int d = 0; d < DP / 32; ++d)
 #pragma unroll
@@ -677,35 +775,56 @@ __global__ __launch_bounds__(256) void attend_many(const AttnLaunch a)
 
 // ---- joining split pieces ---------------------------------------------------------
 
-// One workgroup joins one group: a thread takes eight columns of a row, over all parts in
-// order, so the result does not depend on which part ended first.
+// One workgroup joins up to KVX_JOIN_ROWS rows of a group.  A thread takes eight columns of a row over
+// every kLanes-th part; the threads of a row then add up in a fixed order, so the result
+// does not depend on which part ended first.
 template <class T, int DP>
 __global__ __launch_bounds__(256) void join(const AttnLaunch a)
 {
+    constexpr int kCols = DP / 8, kLanes = 256 / (KVX_JOIN_ROWS * kCols);
+    static_assert(kLanes >= 1, "");
+    __shared__ float share_l[kLanes][KVX_JOIN_ROWS];
+    __shared__ __attribute__((aligned(16))) float share_v[kLanes][KVX_JOIN_ROWS][DP];
     if ((int32_t)blockIdx.x >= a.head->n_groups) return;
     const AttnGroup gr = a.groups[blockIdx.x];
-    for (int c = threadIdx.x; c < gr.rows * (DP / 8); c += 256) {
-        const int row = c / (DP / 8), d = c % (DP / 8) * 8;
-        float top = -INFINITY;
-        for (int k = 0; k < gr.n_parts; ++k)
-            top = fmaxf(top, a.part_ml[2 * ((int64_t)gr.prow + (int64_t)k * gr.stride + row)]);
-        float l = 0.f, v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        for (int k = 0; k < gr.n_parts; ++k) {
-            const int64_t pr = (int64_t)gr.prow + (int64_t)k * gr.stride + row;
-            const float m = a.part_ml[2 * pr];
-            if (m == -INFINITY) continue;  // this part saw nothing
-            const float by = __builtin_amdgcn_exp2f(m - top);
-            l += a.part_ml[2 * pr + 1] * by;
-            const f32x4 x = *(const f32x4 *)(a.part_o + pr * DP + d), y = *(const f32x4 *)(a.part_o + pr * DP + d + 4);
+    const int d = threadIdx.x % kCols * 8, row = threadIdx.x / kCols % KVX_JOIN_ROWS;
+    const int k0 = threadIdx.x / (kCols * KVX_JOIN_ROWS);
+    const bool live = row < gr.rows;
+    const float *ml = a.part_ml + 2 * ((int64_t)gr.prow + (live ? row : 0)), *po =
+        a.part_o + ((int64_t)gr.prow + (live ? row : 0)) * DP + d;
+    float top = -INFINITY;
+#pragma unroll 4
+    for (int k = 0; k < gr.n_parts; ++k) top = fmaxf(top, ml[2 * (int64_t)k * gr.stride]);
+    float l = 0.f, v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 4
+    for (int k = k0; k < gr.n_parts; k += kLanes) {
+        const float *at = ml + 2 * (int64_t)k * gr.stride, *x = po + (int64_t)k * gr.stride * DP;
+        const float m = at[0];
+        const float by = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top);  // saw nothing: zeros
+        l += at[1] * by;
+        const f32x4 p = *(const f32x4 *)x, q = *(const f32x4 *)(x + 4);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] += x[i] * by, v[4 + i] += y[i] * by;
-        }
-        const uint32_t R = (uint32_t)(gr.row0 + row);
-        const int32_t tok = (int32_t)div_by(R, a.group_magic, a.group_shift);
-        const int32_t head = gr.head * a.group + (int32_t)R - tok * a.group;
-        store_out<T>(a, (int64_t)gr.q_begin + tok, head, d, v, l == 0.f ? 0.f : a.v_scale / l);
-        if (d == 0) store_lse(a, (int64_t)gr.q_begin + tok, head, top, l);
+        for (int i = 0; i < 4; ++i) v[i] += p[i] * by, v[4 + i] += q[i] * by;
     }
+    if (kLanes > 1) {
+        if (d == 0) share_l[k0][row] = l;
+        *(f32x4 *)&share_v[k0][row][d] = f32x4{v[0], v[1], v[2], v[3]};
+        *(f32x4 *)&share_v[k0][row][d + 4] = f32x4{v[4], v[5], v[6], v[7]};
+        __syncthreads();
+        if (k0 > 0) return;
+        l = share_l[0][row];
+        for (int k = 1; k < kLanes; ++k) {
+            l += share_l[k][row];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += share_v[k][row][d + i];
+        }
+    }
+    if (!live) return;
+    const uint32_t R = (uint32_t)(gr.row0 + row);
+    const int32_t tok = (int32_t)div_by(R, a.group_magic, a.group_shift);
+    const int32_t head = gr.head * a.group + (int32_t)R - tok * a.group;
+    store_out<T>(a, (int64_t)gr.q_begin + tok, head, d, v, l == 0.f ? 0.f : a.v_scale / l);
+    if (d == 0) store_lse(a, (int64_t)gr.q_begin + tok, head, top, l);
 }
 
 // ---- launches ---------------------------------------------------------------------
@@ -717,17 +836,19 @@ int launch_attend_dim(const AttnLaunch &a, int which, uint32_t grid, hipStream_t
     const bool plain = a.cap_log2 == 0.f && !a.slopes && a.scale_log2 > 0.f;
     const void *fn;
     size_t lds = 0;
+    uint32_t threads = 256;
     if (which == 0) {
         fn = plain ? (const void *)&attend_few<T, E4M3, DP, false> : (const void *)&attend_few<T, E4M3, DP, true>;
     } else {
         fn = plain ? (const void *)&attend_many<T, E4M3, DP, false> : (const void *)&attend_many<T, E4M3, DP, true>;
-        lds = 4 * KVX_TILE_KEYS * DP * sizeof(T);
+        lds = many_lds<DP>();
+        threads = 64 * many_waves<DP>();
         const hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
         if (e != hipSuccess) return (int)e;
     }
     AttnLaunch arg = a;
     void *args[] = {&arg};
-    return (int)hipLaunchKernel(fn, dim3(grid), dim3(256), args, lds, stream);
+    return (int)hipLaunchKernel(fn, dim3(grid), dim3(threads), args, lds, stream);
 }
 
 template <class T>

@@ -53,10 +53,12 @@ int launch_remap(const RemapLaunch &a, hipStream_t stream);
 
 #define KVX_TILE_KEYS 64      // keys of one tile: the unit in which work is counted and split
 #define KVX_ROWS_FEW 16       // rows of a piece of the few-rows kernel
-#define KVX_ROWS_MANY 128     // rows of a piece of the many-rows kernel
 #define KVX_APPEND_TOKENS 16  // new tokens of one append item
-#define KVX_TARGET_FEW 1024   // pieces the few-rows work is split into, about
-#define KVX_TARGET_MANY 512   // pieces the many-rows work is split into, about
+#define KVX_JOIN_ROWS 4       // rows joined by one workgroup
+
+// Rows of a piece of the many-rows kernel: 32 to a wave; at the widest heads a wave's
+// registers leave room for four waves only.
+KVX_HD int32_t rows_many(int dim) { return dim > 128 ? 128 : 256; }
 
 // One workgroup's piece of attention: rows [row0, row0 + rows of the kernel) of one
 // sequence and cache head, over key tiles [tile0, tile1) of the tiles any of its rows sees.
@@ -70,7 +72,8 @@ struct AttnItem {
 };
 static_assert(sizeof(AttnItem) == 48, "");
 
-// Partial results to join: n_parts pieces of `rows` rows, part i at prow + i * stride.
+// Partial results to join: n_parts pieces of `rows` rows (at most KVX_JOIN_ROWS), part i at
+// prow + i * stride.
 struct AttnGroup {
     int32_t prow, n_parts, stride, rows;
     int32_t q_begin, q_len, head, row0;

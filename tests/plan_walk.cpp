@@ -47,6 +47,7 @@ int main()
         d.num_heads = 1 + (int32_t)below(3);
         d.block_size = 16;
         kv_attn_desc a{};
+        d.head_dim = below(2) ? 64 : 256;
         a.num_q_heads = d.num_heads * (1 + (int32_t)below(9));
         const int mode = (int)below(4);
         a.window = mode == 1 || mode == 3 ? 1 + (int32_t)below(300) : 0;
@@ -77,7 +78,7 @@ int main()
         std::map<int32_t, std::tuple<int32_t, int32_t, int32_t>> parts;  // prow -> (q_begin, head, row0)
         for (int cls = 0; cls < 2; ++cls)
             for (const AttnItem &it : cls ? p.many : p.few) {
-                const int step = cls ? KVX_ROWS_MANY : KVX_ROWS_FEW;
+                const int step = cls ? l.rows_many : KVX_ROWS_FEW;
                 CHECK(it.head >= 0 && it.head < d.num_heads && it.row0 % step == 0);
                 const int64_t rows = std::min<int64_t>(step, (int64_t)it.q_len * l.group - it.row0);
                 CHECK(rows > 0);
@@ -107,14 +108,27 @@ int main()
                     }
                 }
             }
+        std::map<int32_t, int32_t> joined;  // prow of a part -> its rows that some record joins
         for (const AttnGroup &g : p.groups)
             for (int k = 0; k < g.n_parts; ++k) {
-                const auto f = parts.find(g.prow + k * g.stride);
-                CHECK(f != parts.end() && f->second == std::make_tuple(g.q_begin, g.head, g.row0));
-                CHECK(g.rows <= g.stride);
-                parts.erase(f);
+                // a record starts at some row of the part
+                auto f = parts.upper_bound(g.prow + k * g.stride);
+                CHECK(f != parts.begin());
+                --f;
+                const int32_t off = g.prow + k * g.stride - f->first;
+                CHECK(off >= 0 && off + g.rows <= g.stride && g.rows >= 1 && g.rows <= KVX_JOIN_ROWS);
+                CHECK(f->second == std::make_tuple(g.q_begin, g.head, g.row0 - off));
+                CHECK(joined[f->first] == off);
+                joined[f->first] += g.rows;
             }
-        CHECK(parts.empty());
+        for (int cls = 0; cls < 2; ++cls)
+            for (const AttnItem &it : cls ? p.many : p.few)
+                if (it.prow >= 0) {
+                    const int64_t rows = std::min<int64_t>(cls ? l.rows_many : KVX_ROWS_FEW,
+                                                           (int64_t)it.q_len * l.group - it.row0);
+                    CHECK(joined[it.prow] == rows);
+                }
+        CHECK(joined.size() == parts.size());
         std::set<std::pair<const int32_t *, int>> appended;
         for (const AppendItem &it : p.append)
             for (int k = 0; k < it.count; ++k) CHECK(appended.emplace(it.table, it.pos + k).second);
