@@ -133,6 +133,14 @@ __device__ __forceinline__ typename Vec<T>::x4 read_column(const T *p)
     return __builtin_bit_cast(typename Vec<T>::x4, v);
 }
 
+// The larger of a lane's value and that of the lane 32 away, on the vector pipe.
+__device__ __forceinline__ float max_of_halves(float x)
+{
+    const uint32_t u = __builtin_bit_cast(uint32_t, x);
+    const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return fmaxf(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
+}
+
 // The keys one query sees, as two stretches: [0, prefix) and [low, high].  Compared without
 // branches: a mask is three compares and a select.
 struct RowMask {
@@ -531,33 +539,37 @@ __global__ __launch_bounds__(256) void attend_few(const AttnLaunch a)
 template <int DP>
 constexpr int many_waves() { return DP == 256 ? 4 : 8; }
 
+// Shared memory: two tiles of keys and of values, and the row offsets of four tiles.
 template <int DP>
-constexpr int many_lds() { return 2 * KVX_TILE_KEYS * (key_row<DP>() + value_row<DP>()) * 2; }
+constexpr int many_lds() { return KVX_TILE_KEYS * (2 * (key_row<DP>() + value_row<DP>()) * 2 + 4 * 8); }
 
 // 32 rows a wave (32x32x16 products); the workgroup's waves share 64-key tiles of K and V in
-// shared memory, two deep; while one is worked on, the next one is on its way to registers (and
-// the block ids of the one after it).
+// shared memory, two deep.  While tile i is worked on, tile i + 1, which has arrived in
+// registers, goes to shared memory, tile i + 2 is sent for, the places of its rows having been
+// worked out an iteration before by one wave for all (a lane a key), and the block ids of tile i + 4
+// are fetched by another.  One barrier a tile.
 template <class T, bool E4M3, int DP, bool SHAPED>
 __global__ __launch_bounds__(64 * many_waves<DP>()) void attend_many(const AttnLaunch a)
 {
     typedef typename Vec<T>::x8 T8;
     typedef typename Vec<T>::x4 T4;
-    typedef typename Vec<T>::x2 T2;
     constexpr int kWaves = many_waves<DP>();
     constexpr int N = KVX_TILE_KEYS;
     constexpr int kRow = DP / 8;                      // pieces of one key row: eight values each
     constexpr int kLoads = N * kRow / (64 * kWaves);  // loads of a thread for one tile of K or V
     static_assert(kLoads * 64 * kWaves == N * kRow, "whole loads");
+    constexpr int kK = key_row<DP>(), kV = value_row<DP>();
     extern __shared__ __attribute__((aligned(16))) char shared[];
-    constexpr int kK = key_row<DP>(), kV = value_row<DP>(), kTile = N * (kK + kV);
-    T *const tiles = (T *)shared;  // [2]: K [N][kK], V [N][kV]
-    __shared__ int32_t odd[2];     // one past the last tile of this buffer with infinities or NaN in V
+    T *const keys = (T *)shared, *const values = keys + 2 * N * kK;  // [2][N][kK], [2][N][kV]
+    int64_t *const offs = (int64_t *)(values + 2 * N * kV);          // [4][N]
+    __shared__ int32_t odd[2];  // one past the last tile (of either parity) with infinities or NaN in V
 
     if ((int32_t)blockIdx.x >= a.head->n_many) return;
     const Piece s = load_piece<32 * kWaves>(a);
+    const int32_t n_tiles = s.tile1 - s.tile0;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int n = lane & 31, g = lane >> 5;
-    const int rw = wave * 32 + n;              // the lane's row of the piece
+    const int rw = wave * 32 + n;  // the lane's row of the piece
 
     const uint32_t R = (uint32_t)(s.row0 + (rw < s.rows ? rw : s.rows - 1));
     const int32_t tok = (int32_t)div_by(R, a.group_magic, a.group_shift);
@@ -580,39 +592,68 @@ __global__ __launch_bounds__(64 * many_waves<DP>()) void attend_many(const AttnL
     const float sc = SHAPED ? 1.f : a.scale_log2;
     const float slack = 8.f / sc;  // a maximum that grows by less than 2^8 is not worth a rescaling
 
-    // The thread's pieces of a tile: eight values of key rows row0 + c * kApart.
+    // The thread's pieces of a tile: eight values of key rows krow + c * kApart.
     typedef typename std::conditional<E4M3, u32x2, u32x4>::type Piece8;
     constexpr int kApart = 64 * kWaves / kRow;
     const int krow = threadIdx.x / kRow, chunk = threadIdx.x % kRow;
     const bool inside = chunk * 8 < a.dim;  // columns past the rows' width are zeros
-    int32_t blk[kLoads];
     Piece8 kr[kLoads], vr[kLoads];
 #pragma unroll
     for (int c = 0; c < kLoads; ++c) kr[c] = vr[c] = Piece8{};
-    auto look_up = [&](int32_t i) __attribute__((always_inline)) {
-        const int32_t j0 = s.walk.start(i) + krow;
-#pragma unroll
-        for (int c = 0; c < kLoads; ++c) blk[c] = block_of(a, s, seen_key(s, j0 + c * kApart));
-    };
-    auto load = [&](int32_t i) __attribute__((always_inline)) {
-        const int32_t j0 = s.walk.start(i) + krow;
+    auto load = [&](Piece8(&r)[kLoads], const uint8_t *base, int32_t i) __attribute__((always_inline)) {
 #pragma unroll
         for (int c = 0; c < kLoads; ++c) {
-            const int64_t off = key_offset(a, s, seen_key(s, j0 + c * kApart), blk[c]) + chunk * (int)sizeof(Piece8);
-            if (inside) {
-                kr[c] = *(const KVX_GLOBAL Piece8 *)(a.k_base + off);
-                vr[c] = *(const KVX_GLOBAL Piece8 *)(a.v_base + off);
-            }
+            const int64_t off = offs[(i & 3) * N + krow + c * kApart] + chunk * (int)sizeof(Piece8);
+            if (inside) r[c] = *(const KVX_GLOBAL Piece8 *)(base + off);
         }
     };
     auto widen = [&](const Piece8 &r) __attribute__((always_inline)) {
         if constexpr (E4M3) return __builtin_shufflevector(from_e4m3<T>(r[0]), from_e4m3<T>(r[1]), 0, 1, 2, 3, 4, 5, 6, 7);
         else return __builtin_bit_cast(T8, r);
     };
+    auto start = [&](int32_t i) __attribute__((always_inline)) { return s.walk.start(s.tile0 + i); };
+    auto partly = [&](int32_t i) __attribute__((always_inline)) { return !all_see(a, s, start(i), N); };
+    // rows' places: the lane's key of tile i
+    auto find = [&](int32_t i) __attribute__((always_inline)) { return block_of(a, s, seen_key(s, start(i) + lane)); };
+    auto place = [&](int32_t i, int32_t blk) __attribute__((always_inline)) {
+        offs[(i & 3) * N + lane] = key_offset(a, s, seen_key(s, start(i) + lane), blk);
+    };
+    auto put_keys = [&](int32_t i) __attribute__((always_inline)) {
+#pragma unroll
+        for (int c = 0; c < kLoads; ++c)
+            *(T8 *)(keys + ((i & 1) * N + krow + c * kApart) * kK + chunk * 8) = widen(kr[c]);
+    };
+    auto put_values = [&](int32_t i) __attribute__((always_inline)) {
+        T *V = values + (i & 1) * N * kV;
+#pragma unroll
+        for (int c = 0; c < kLoads; ++c) *(T8 *)(V + (krow + c * kApart) * kV + chunk * 8) = widen(vr[c]);
+        if (partly(i)) {
+            bool any = false;
+#pragma unroll
+            for (int c = 0; c < kLoads; ++c) any |= any_not_finite<T>(widen(vr[c]));
+            if (any) odd[i & 1] = i + 1;
+        }
+    };
+    int32_t blk = 0;
+    // Before tile i is worked on.
+    auto stage = [&](int32_t i) __attribute__((always_inline)) {
+        if (i + 1 < n_tiles) {
+            put_keys(i + 1);
+            put_values(i + 1);
+        }
+        if (i + 2 < n_tiles) {
+            load(kr, a.k_base, i + 2);
+            load(vr, a.v_base, i + 2);
+        }
+        if ((i + 3) % kWaves == wave && i + 3 < n_tiles) place(i + 3, blk);
+        if ((i + 4) % kWaves == wave && i + 4 < n_tiles) blk = find(i + 4);
+    };
 
-    // one tile's products for the wave's rows
-    auto work = [&](const T *K, const T *V, int32_t j0, bool masked) __attribute__((always_inline)) {
-        f32x16 x[2];
+    f32x16 x[2];
+    T8 w[4];  // the weights of 16 keys each
+    // register r of x[t]: key 32 t + 8 (r / 4) + 4 g + r mod 4
+    auto scores = [&](int32_t i) __attribute__((always_inline)) {
+        const T *K = keys + ((i & 1) * N + n) * kK + 8 * g;
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -621,7 +662,18 @@ __global__ __launch_bounds__(64 * many_waves<DP>()) void attend_many(const AttnL
         for (int c = 0; c < DP / 16; ++c)
 #pragma unroll
             for (int t = 0; t < 2; ++t) x[t] = mfma32(*(const T8 *)(K + 32 * t * kK + 16 * c), q[c], x[t]);
-        // register r of tile t: key 32 t + 8 (r / 4) + 4 g + r mod 4
+        // reads run kAhead ahead of the products that use them; left to itself the compiler waits
+        // for each one
+        constexpr int kReads = DP / 8, kAhead = kReads < 8 ? kReads : 8;
+        __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+        for (int c = 0; c < kReads - kAhead; ++c) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 0);
+    };
+    auto weights = [&](int32_t j0, bool masked) __attribute__((always_inline)) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             auto key = [&](int r) { return j0 + 32 * t + 8 * (r >> 2) + 4 * g + (r & 3); };
@@ -633,7 +685,7 @@ __global__ __launch_bounds__(64 * many_waves<DP>()) void attend_many(const AttnL
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int r = 0; r < 16; ++r) mx = fmaxf(mx, x[t][r]);
-        mx = fmaxf(mx, __shfl_xor(mx, 32));
+        mx = max_of_halves(mx);
         if (__any(mx > m + slack || (m == -INFINITY && mx > m))) {
             const float up = fmaxf(m, mx);
             const float by = up == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - up) * sc);
@@ -643,7 +695,6 @@ __global__ __launch_bounds__(64 * many_waves<DP>()) void attend_many(const AttnL
             for (int d = 0; d < DP / 32; ++d) o[d] *= by;
         }
         const float mm = m == -INFINITY ? 0.f : m * sc;
-        T8 w[4];  // the weights of 16 keys each
         float sum[2] = {0.f, 0.f};
 #pragma unroll
         for (int t = 0; t < 2; ++t)
@@ -657,86 +708,85 @@ __global__ __launch_bounds__(64 * many_waves<DP>()) void attend_many(const AttnL
                 w[2 * t + (r >> 3)][(r & 7) + 1] = (T)e1;
             }
         l += sum[0] + sum[1];
-        // V^T of 16 keys: slots 0-3 are keys 4 g + 0..3, slots 4-7 keys 8 + 4 g + 0..3
-        auto value = [&](int d, int u) {
-            const T4 lo = read_column<T>(V + 16 * u * kV + 32 * d), hi = read_column<T>(V + (16 * u + 8) * kV + 32 * d);
-            return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-        };
+    };
+    // V^T of 16 keys: slots 0-3 are keys 4 g + 0..3, slots 4-7 keys 8 + 4 g + 0..3
+    auto add_values = [&](int32_t i) __attribute__((always_inline)) {
+        const T *V = values + ((i & 1) * N + 4 * g + ((lane & 15) >> 2)) * kV + ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
 #pragma unroll
         for (int u = 0; u < 4; ++u)
 #pragma unroll
-            for (int d = 0; d < DP / 32; ++d) o[d] = mfma32(value(d, u), w[u], o[d]);
+            for (int d = 0; d < DP / 32; ++d) {
+                const T4 lo = read_column<T>(V + 16 * u * kV + 32 * d), hi = read_column<T>(V + (16 * u + 8) * kV + 32 * d);
+                o[d] = mfma32(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7), w[u], o[d]);
+            }
     };
-
     // Infinities and NaN among the values of a tile that some rows see in part: a zero weight would
-    // turn them into NaN in rows that do not see them.  The tile's copy for the product holds
-    // zeros in their place; here each row adds those it sees, from the tile as it was (in `was`).
-    auto add_specials = [&](const T *was, int32_t j0) __attribute__((always_inline)) {
-#pragma unroll 1
-        for (int k = 0; k < N; ++k) {
-            const bool seen = mask.sees(j0 + k);
+    // turn them into NaN in rows that do not see them.  Before tile i is worked on it is read
+    // again; its copy for the product gets zeros in their place, and each row adds those it sees from
+    // a copy as it was, in the space of tile i + 1, which is put there afterwards.
+    auto specials = [&](int32_t i, auto rows) __attribute__((always_inline)) {
+        Piece8 r[kLoads];
 #pragma unroll
-            for (int d = 0; d < DP / 32; ++d)
+        for (int c = 0; c < kLoads; ++c) r[c] = Piece8{};
+        load(r, a.v_base, i);
+        T *V = values + (i & 1) * N * kV, *was = values + ((i + 1) & 1) * N * kV;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const T4 v = *(const T4 *)(was + k * kV + 32 * d + 8 * r + 4 * g);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        o[d][4 * r + e] += seen && not_finite<T>(__builtin_bit_cast(uint16_t, v[e])) ? (float)v[e] : 0.f;
-                }
+        for (int c = 0; c < kLoads; ++c) {
+            const T8 v = widen(r[c]);
+            *(T8 *)(was + (krow + c * kApart) * kV + chunk * 8) = v;
+            *(T8 *)(V + (krow + c * kApart) * kV + chunk * 8) = only_finite<T>(v);
         }
+        __syncthreads();
+        if (decltype(rows)::value) {
+#pragma unroll 1
+            for (int k = 0; k < N; ++k) {
+                const bool seen = mask.sees(start(i) + k);
+#pragma unroll
+                for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const T4 v = *(const T4 *)(was + k * kV + 32 * d + 8 * b + 4 * g);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            o[d][4 * b + e] +=
+                                seen && not_finite<T>(__builtin_bit_cast(uint16_t, v[e])) ? (float)v[e] : 0.f;
+                    }
+            }
+        }
+        __syncthreads();
     };
 
     if (threadIdx.x < 2) odd[threadIdx.x] = 0;
+    for (int32_t i = 0; i < 3 && i < n_tiles; ++i)
+        if (i % kWaves == wave) place(i, find(i));
+    if (3 % kWaves == wave && 3 < n_tiles) blk = find(3);
     __syncthreads();
-    if (s.tile0 < s.tile1) {
-        look_up(s.tile0);
-        load(s.tile0);
-        if (s.tile0 + 1 < s.tile1) look_up(s.tile0 + 1);
+    if (n_tiles > 0) {
+        load(kr, a.k_base, 0);
+        load(vr, a.v_base, 0);
+        put_keys(0);
+        put_values(0);
+        if (1 < n_tiles) {
+            load(kr, a.k_base, 1);
+            load(vr, a.v_base, 1);
+        }
     }
-    // Puts tile i, which has arrived, into shared memory and sends for the next one.
-    auto stage = [&](int32_t i, bool masked, auto rows) __attribute__((always_inline)) {
-        const int buf = (i - s.tile0) & 1;
-        T *K = tiles + buf * kTile, *V = K + N * kK;
-#pragma unroll
-        for (int c = 0; c < kLoads; ++c) {
-            *(T8 *)(K + (krow + c * kApart) * kK + chunk * 8) = widen(kr[c]);
-            *(T8 *)(V + (krow + c * kApart) * kV + chunk * 8) = widen(vr[c]);
-        }
-        if (masked) {
-            bool any = false;
-#pragma unroll
-            for (int c = 0; c < kLoads; ++c) any |= any_not_finite<T>(widen(vr[c]));
-            if (any) odd[buf] = i + 1;
-        }
-        __syncthreads();  // the tile is whole; and no wave still works on the other one
-        if (__builtin_expect(masked && odd[buf] == i + 1, 0)) {
-            T *was = tiles + (buf ^ 1) * kTile + N * kK;
-#pragma unroll
-            for (int c = 0; c < kLoads; ++c) {
-                const T8 v = widen(vr[c]);
-                *(T8 *)(was + (krow + c * kApart) * kV + chunk * 8) = v;
-                *(T8 *)(V + (krow + c * kApart) * kV + chunk * 8) = only_finite<T>(v);
-            }
-            __syncthreads();
-            if (decltype(rows)::value) add_specials(was, s.walk.start(i));
-            __syncthreads();  // before the next tile takes its place
-        }
-        if (i + 1 < s.tile1) load(i + 1);
-        if (i + 2 < s.tile1) look_up(i + 2);
-    };
-    auto partly = [&](int32_t i) { return !all_see(a, s, s.walk.start(i), N); };
+    __syncthreads();
     if (wave * 32 >= s.rows) {  // a wave without rows only helps loading
-        for (int32_t i = s.tile0; i < s.tile1; ++i) stage(i, partly(i), std::false_type{});
+        for (int32_t i = 0; i < n_tiles; ++i) {
+            if (__builtin_expect(odd[i & 1] == i + 1, 0)) specials(i, std::false_type{});
+            stage(i);
+            __syncthreads();
+        }
         return;
     }
-    const int kat = n * kK + 8 * g;
-    const int vat = N * kK + (4 * g + ((lane & 15) >> 2)) * kV + ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
-    for (int32_t i = s.tile0; i < s.tile1; ++i) {
-        const bool masked = partly(i);
-        stage(i, masked, std::true_type{});
-        const T *tile = tiles + ((i - s.tile0) & 1) * kTile;
-        work(tile + kat, tile + vat, s.walk.start(i), masked);
+    for (int32_t i = 0; i < n_tiles; ++i) {
+        if (__builtin_expect(odd[i & 1] == i + 1, 0)) specials(i, std::true_type{});
+        stage(i);
+        scores(i);
+        weights(start(i), partly(i));
+        add_values(i);
+        __syncthreads();
     }
     l += __shfl_xor(l, 32);
     if (rw >= s.rows) return;

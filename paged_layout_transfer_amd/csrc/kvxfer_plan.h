@@ -3,6 +3,7 @@
 // vectors have their capacity).
 #pragma once
 #include <algorithm>
+#include <functional>
 #include <vector>
 
 #include "kvxfer_ops.h"
@@ -20,8 +21,15 @@ struct PlanLimits {
     int64_t cap_few, cap_many, cap_groups, cap_append, cap_prows;
 };
 
-// Capacities that hold any plan of max_seqs sequences and max_tokens new tokens.  Splitting
-// makes at most 2 * slots pieces of a class (split_class), each with its rows in the workspace.
+// Capacities that hold any plan of max_seqs sequences and max_tokens new tokens.  Of a class
+// with at most `pieces` pieces, split_class cuts at most cut_parts() parts, and makes at most all_parts()
+// parts in all.
+inline int64_t cut_parts(int64_t pieces, int64_t slots) { return pieces <= slots ? slots : 4 * slots; }
+inline int64_t all_parts(int64_t pieces, int64_t slots)
+{
+    return pieces <= slots ? slots : std::max(4 * slots, pieces + 2 * slots);
+}
+
 inline PlanLimits plan_limits(const kv_pool_desc &d, const kv_attn_desc &a)
 {
     PlanLimits l;
@@ -33,14 +41,19 @@ inline PlanLimits plan_limits(const kv_pool_desc &d, const kv_attn_desc &a)
     l.slots_few = slots_few(d.head_dim);
     const int64_t rows = a.max_tokens * l.group;
     const int64_t seqs = std::min<int64_t>(a.max_seqs, a.max_tokens);
-    const bool many = rows > KVX_ROWS_FEW;
-    l.cap_few = seqs * l.heads + 2 * l.slots_few;
-    l.cap_many = many ? (rows / l.rows_many + seqs) * l.heads + 2 * kSlotsMany : 0;
-    const int64_t few_rows = std::min<int64_t>(rows, KVX_ROWS_FEW), many_rows = std::min<int64_t>(rows, l.rows_many);
-    l.cap_groups = l.slots_few * ((few_rows + KVX_JOIN_ROWS - 1) / KVX_JOIN_ROWS) +
-                   (many ? kSlotsMany * ((many_rows + KVX_JOIN_ROWS - 1) / KVX_JOIN_ROWS) : 0);
+    auto slices = [](int64_t n) { return (n + KVX_JOIN_ROWS - 1) / KVX_JOIN_ROWS; };
+    const int64_t few = seqs * l.heads, cut_few = cut_parts(few, l.slots_few);
+    l.cap_few = all_parts(few, l.slots_few);
+    l.cap_groups = cut_few / 2 * slices(std::min<int64_t>(rows, KVX_ROWS_FEW));
+    l.cap_prows = cut_few * KVX_ROWS_FEW;
+    l.cap_many = 0;
+    if (rows > KVX_ROWS_FEW) {
+        const int64_t many = (rows / l.rows_many + seqs) * l.heads, cut_many = cut_parts(many, kSlotsMany);
+        l.cap_many = all_parts(many, kSlotsMany);
+        l.cap_groups += cut_many / 2 * slices(std::min<int64_t>(rows, l.rows_many));
+        l.cap_prows += cut_many * l.rows_many;
+    }
     l.cap_append = a.max_tokens / KVX_APPEND_TOKENS + seqs;
-    l.cap_prows = 2 * l.slots_few * KVX_ROWS_FEW + (many ? 2 * kSlotsMany * l.rows_many : 0);
     return l;
 }
 
@@ -53,6 +66,7 @@ struct Plan {
     bool appendable = true;   // every sequence has q_len <= kv_len
     // scratch
     std::vector<AttnItem> whole;
+    std::vector<int64_t> parts, ends;
 
     void reserve(const PlanLimits &l)
     {
@@ -61,49 +75,103 @@ struct Plan {
         whole.reserve(std::max(l.cap_few, l.cap_many));
         groups.reserve(l.cap_groups);
         append.reserve(l.cap_append);
+        parts.reserve(8 * (size_t)std::max(l.slots_few, kSlotsMany));
+        ends.reserve((size_t)std::max(l.slots_few, kSlotsMany));
     }
 };
 
-// Splits the pieces in `whole` (tile0 = 0, tile1 = all tiles) over the keys.  Fewer pieces than
-// workgroups that run at once: the smallest share of tiles whose cuts do not outnumber them, so
-// that all run in one go; otherwise only pieces longer than the even share are cut.  Either way no more
-// than 2 * slots parts are cut: a piece of t tiles gives at most t / share + 1 <= 2 t / share, and the
-// sum of t / share is at most slots.  A part shorter than min_tiles is not worth its partial
-// result's trip.
+// Parts that `share` tiles at most cut the pieces into, all cache heads together.
+inline int64_t parts_at(const std::vector<AttnItem> &whole, int64_t share, int32_t heads)
+{
+    int64_t n = 0;
+    for (const AttnItem &it : whole) n += std::max<int64_t>(1, (it.tile1 + share - 1) / share);
+    return n * heads;
+}
+
+// When the last of `slots` workgroups ends, in tiles, if each takes the longest part left; a
+// part costs its tiles and one more for its start and end.  `ends` is scratch.
+inline int64_t span_at(const std::vector<AttnItem> &whole, int64_t share, int64_t slots, std::vector<int64_t> &parts,
+                       std::vector<int64_t> &ends)
+{
+    parts.clear();
+    for (const AttnItem &it : whole) {
+        const int64_t n = std::max<int64_t>(1, (it.tile1 + share - 1) / share);
+        for (int64_t k = 0; k < n; ++k) parts.push_back(it.tile1 * (k + 1) / n - it.tile1 * k / n + 1);
+    }
+    std::sort(parts.begin(), parts.end(), std::greater<int64_t>());
+    ends.assign((size_t)slots, 0);  // a heap, the earliest end first
+    for (int64_t p : parts) {
+        std::pop_heap(ends.begin(), ends.end(), std::greater<int64_t>());
+        ends.back() += p;
+        std::push_heap(ends.begin(), ends.end(), std::greater<int64_t>());
+    }
+    return *std::max_element(ends.begin(), ends.end());
+}
+
+// Splits the pieces in `whole` (tile0 = 0, tile1 = all tiles, one for all cache heads) over the keys.
+//  * At most as many pieces as workgroups that run at once (slots): the smallest share of tiles
+//    whose parts do not outnumber them, so that all run in one go.
+//  * At least four times as many: only pieces longer than the even share are cut; the rest
+//    even out by themselves, longest first.
+//  * In between, where a last round of a few whole pieces would leave most of the chip idle:
+//    no cut, or the smallest share whose parts fill two, three or four rounds, whichever ends first.
+// At most 4 * slots parts in the first and last case; in the second a piece of t > share tiles
+// gives at most t / share + 1 < 2 t / share parts, and the sum of t / share is at most slots.
+// A part shorter than min_tiles is not worth its partial result's trip.
 inline void split_class(Plan &p, std::vector<AttnItem> &out, const PlanLimits &l, int32_t rows_of_piece,
                         int64_t slots, int64_t min_tiles, int64_t *prow)
 {
-    int64_t total = 0, longest = 0;
-    for (const AttnItem &it : p.whole) total += it.tile1, longest = std::max<int64_t>(longest, it.tile1);
-    int64_t share = std::max(min_tiles, (total + slots - 1) / slots);
-    if ((int64_t)p.whole.size() < slots) {
-        int64_t hi = std::max(share, longest);  // no cut at all: fits
-        while (share < hi) {
-            const int64_t mid = (share + hi) / 2;
-            int64_t n = 0;
-            for (const AttnItem &it : p.whole) n += std::max<int64_t>(1, (it.tile1 + mid - 1) / mid);
-            if (n <= slots) hi = mid;
-            else share = mid + 1;
+    int64_t total = 0, longest = 1;
+    for (const AttnItem &it : p.whole)
+        total += (int64_t)it.tile1 * l.heads, longest = std::max<int64_t>(longest, it.tile1);
+    const int64_t even = std::max(min_tiles, (total + slots - 1) / slots);
+    const int64_t pieces = (int64_t)p.whole.size() * l.heads;
+    auto fitting = [&](int64_t parts) {
+        int64_t lo = std::min(even, longest), hi = longest;
+        if (parts > slots) lo = std::min(min_tiles, longest);
+        while (lo < hi) {
+            const int64_t mid = (lo + hi) / 2;
+            if (parts_at(p.whole, mid, l.heads) <= parts) hi = mid;
+            else lo = mid + 1;
+        }
+        return lo;
+    };
+    int64_t share = longest;
+    if (pieces <= slots) {
+        share = fitting(slots);
+    } else if (pieces >= 4 * slots) {
+        share = std::min(even, longest);
+    } else {
+        const int64_t lanes = std::max<int64_t>(1, slots / l.heads);
+        int64_t best = span_at(p.whole, longest, lanes, p.parts, p.ends);
+        for (int64_t rounds = 2; rounds <= 4; ++rounds) {
+            if (pieces > rounds * slots) continue;
+            const int64_t s = fitting(rounds * slots), span = span_at(p.whole, s, lanes, p.parts, p.ends);
+            // a split costs a trip through the workspace: only for a twentieth of the time
+            if (span * 20 < best * 19) best = span, share = s;
         }
     }
     for (const AttnItem &it : p.whole) {
         const int64_t n = (it.tile1 + share - 1) / share;
-        if (n <= 1) {
-            out.push_back(it);
-            continue;
-        }
         const int32_t rows = (int32_t)std::min<int64_t>(rows_of_piece, (int64_t)it.q_len * l.group - it.row0);
-        for (int32_t r = 0; r < rows; r += KVX_JOIN_ROWS)
-            p.groups.push_back(AttnGroup{(int32_t)*prow + r, (int32_t)n, rows_of_piece,
-                                         std::min(KVX_JOIN_ROWS, rows - r), it.q_begin, it.q_len, it.head,
-                                         it.row0 + r});
-        for (int64_t k = 0; k < n; ++k) {
+        for (int32_t head = 0; head < l.heads; ++head) {
             AttnItem part = it;
-            part.tile0 = (int32_t)(it.tile1 * k / n);
-            part.tile1 = (int32_t)(it.tile1 * (k + 1) / n);
-            part.prow = (int32_t)*prow;
-            *prow += rows_of_piece;
-            out.push_back(part);
+            part.head = head;
+            if (n <= 1) {
+                out.push_back(part);
+                continue;
+            }
+            for (int32_t r = 0; r < rows; r += KVX_JOIN_ROWS)
+                p.groups.push_back(AttnGroup{(int32_t)*prow + r, (int32_t)n, rows_of_piece,
+                                             std::min(KVX_JOIN_ROWS, rows - r), it.q_begin, it.q_len, head,
+                                             it.row0 + r});
+            for (int64_t k = 0; k < n; ++k) {
+                part.tile0 = (int32_t)(it.tile1 * k / n);
+                part.tile1 = (int32_t)(it.tile1 * (k + 1) / n);
+                part.prow = (int32_t)*prow;
+                *prow += rows_of_piece;
+                out.push_back(part);
+            }
         }
     }
     // longest first, so that the last workgroups to start are the short ones
@@ -145,7 +213,7 @@ inline void build_plan(Plan &p, const PlanLimits &l, const kv_seq *seqs, int32_t
                 it.row0 = (int32_t)r;
                 it.tile1 = w.n_tiles;
                 it.prow = -1;
-                for (it.head = 0; it.head < l.heads; ++it.head) p.whole.push_back(it);
+                p.whole.push_back(it);
             }
         }
         split_class(p, few ? p.few : p.many, l, step, few ? l.slots_few : kSlotsMany, few ? 2 : 4, &prow);
