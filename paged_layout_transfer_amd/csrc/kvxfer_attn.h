@@ -159,9 +159,8 @@ struct Piece {
 };
 
 template <int ROWS>
-__device__ __forceinline__ Piece load_piece(const AttnLaunch &a)
+__device__ __forceinline__ Piece piece_of(const AttnLaunch &a, const AttnItem &it)
 {
-    const AttnItem it = a.items[blockIdx.x];
     Piece s;
     s.table = it.table;
     s.kv_len = it.kv_len;
@@ -229,10 +228,12 @@ template <int N, class X, class Key>
 __device__ __forceinline__ void shape(const AttnLaunch &a, X &x, float slope_log2, int32_t p, Key key)
 {
     if (a.cap_log2 != 0.f) {
+        // c tanh y = c - 2 c / (e^2y + 1); the scale makes 2^x of it e^2y.  The reciprocal is good to
+        // one unit in the last place: 2^-23 of the cap.
 #pragma unroll
-        for (int i = 0; i < N; ++i)  // tanh y = 1 - 2 / (e^2y + 1)
-            x[i] = a.cap_log2 *
-                   (1.f - 2.f / (__builtin_amdgcn_exp2f(x[i] * a.scale_log2 * 2.8853900817779268f) + 1.f));
+        for (int i = 0; i < N; ++i)
+            x[i] = __builtin_fmaf(-2.f * a.cap_log2, __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(x[i] * a.scale_log2) + 1.f),
+                                  a.cap_log2);
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i) x[i] *= a.scale_log2;
@@ -297,7 +298,7 @@ __device__ __forceinline__ void store_lse(const AttnLaunch &a, int64_t row, int3
 // slice of shared memory of the wave's own, both loaded a step ahead and their block ids two, with
 // no barrier in the loop.
 template <class T, bool E4M3, int DP, bool SHAPED>
-__global__ __launch_bounds__(256) void attend_few(const AttnLaunch a)
+__global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_few(const AttnLaunch a)
 {
     typedef typename Vec<T>::x8 T8;
     typedef typename Vec<T>::x4 T4;
@@ -311,8 +312,10 @@ __global__ __launch_bounds__(256) void attend_few(const AttnLaunch a)
     __shared__ __attribute__((aligned(16))) char shared[4 * kSlice];
     __shared__ float join_m[4][16], join_l[4][16];
 
+    // the record is read before the count is known: the array holds one for every workgroup
+    const AttnItem it = a.items[blockIdx.x];
     if ((int32_t)blockIdx.x >= a.head->n_few) return;
-    const Piece s = load_piece<16>(a);
+    const Piece s = piece_of<16>(a, it);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int n = lane & 15, g = lane >> 4;
     T *tile = (T *)(shared + wave * kSlice);
@@ -564,8 +567,9 @@ __global__ __launch_bounds__(64 * many_waves<DP>()) void attend_many(const AttnL
     int64_t *const offs = (int64_t *)(values + 2 * N * kV);          // [4][N]
     __shared__ int32_t odd[2];  // one past the last tile (of either parity) with infinities or NaN in V
 
+    const AttnItem it = a.items[blockIdx.x];
     if ((int32_t)blockIdx.x >= a.head->n_many) return;
-    const Piece s = load_piece<32 * kWaves>(a);
+    const Piece s = piece_of<32 * kWaves>(a, it);
     const int32_t n_tiles = s.tile1 - s.tile0;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int n = lane & 31, g = lane >> 5;
@@ -825,48 +829,55 @@ __global__ __launch_bounds__(64 * many_waves<DP>()) void attend_many(const AttnL
 
 // ---- joining split pieces ---------------------------------------------------------
 
-// One workgroup joins up to KVX_JOIN_ROWS rows of a group.  A thread takes eight columns of a row over
-// every kLanes-th part; the threads of a row then add up in a fixed order, so the result
-// does not depend on which part ended first.
+// One workgroup joins up to KVX_JOIN_ROWS rows of a group.  A thread takes eight columns of a
+// row over every kLanes-th part, in one pass with its own running maximum; the threads of a row then
+// add up in a fixed order, so the result does not depend on which part ended first.
 template <class T, int DP>
 __global__ __launch_bounds__(256) void join(const AttnLaunch a)
 {
     constexpr int kCols = DP / 8, kLanes = 256 / (KVX_JOIN_ROWS * kCols);
     static_assert(kLanes >= 1, "");
-    __shared__ float share_l[kLanes][KVX_JOIN_ROWS];
+    __shared__ float share_m[kLanes][KVX_JOIN_ROWS], share_l[kLanes][KVX_JOIN_ROWS];
     __shared__ __attribute__((aligned(16))) float share_v[kLanes][KVX_JOIN_ROWS][DP];
-    if ((int32_t)blockIdx.x >= a.head->n_groups) return;
     const AttnGroup gr = a.groups[blockIdx.x];
+    if ((int32_t)blockIdx.x >= a.head->n_groups) return;
     const int d = threadIdx.x % kCols * 8, row = threadIdx.x / kCols % KVX_JOIN_ROWS;
     const int k0 = threadIdx.x / (kCols * KVX_JOIN_ROWS);
     const bool live = row < gr.rows;
-    const float *ml = a.part_ml + 2 * ((int64_t)gr.prow + (live ? row : 0)), *po =
-        a.part_o + ((int64_t)gr.prow + (live ? row : 0)) * DP + d;
-    float top = -INFINITY;
-#pragma unroll 4
-    for (int k = 0; k < gr.n_parts; ++k) top = fmaxf(top, ml[2 * (int64_t)k * gr.stride]);
-    float l = 0.f, v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    const int64_t first = (int64_t)gr.prow + (live ? row : 0);
+    float m = -INFINITY, l = 0.f, v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll 4
     for (int k = k0; k < gr.n_parts; k += kLanes) {
-        const float *at = ml + 2 * (int64_t)k * gr.stride, *x = po + (int64_t)k * gr.stride * DP;
-        const float m = at[0];
-        const float by = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top);  // saw nothing: zeros
-        l += at[1] * by;
-        const f32x4 p = *(const f32x4 *)x, q = *(const f32x4 *)(x + 4);
+        const int64_t at = first + (int64_t)k * gr.stride;
+        const float pm = a.part_ml[2 * at], pl = a.part_ml[2 * at + 1];
+        const f32x4 x = *(const f32x4 *)(a.part_o + at * DP + d), y = *(const f32x4 *)(a.part_o + at * DP + d + 4);
+        const float up = fmaxf(m, pm);
+        // a part that saw nothing holds zeros and no maximum
+        const float was = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - up);
+        const float by = pm == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(pm - up);
+        m = up;
+        l = l * was + pl * by;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] += p[i] * by, v[4 + i] += q[i] * by;
+        for (int i = 0; i < 4; ++i) v[i] = v[i] * was + x[i] * by, v[4 + i] = v[4 + i] * was + y[i] * by;
     }
     if (kLanes > 1) {
-        if (d == 0) share_l[k0][row] = l;
+        if (d == 0) share_m[k0][row] = m, share_l[k0][row] = l;
         *(f32x4 *)&share_v[k0][row][d] = f32x4{v[0], v[1], v[2], v[3]};
         *(f32x4 *)&share_v[k0][row][d + 4] = f32x4{v[4], v[5], v[6], v[7]};
         __syncthreads();
         if (k0 > 0) return;
-        l = share_l[0][row];
-        for (int k = 1; k < kLanes; ++k) {
-            l += share_l[k][row];
+        m = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += share_v[k][row][d + i];
+        for (int k = 0; k < kLanes; ++k) m = fmaxf(m, share_m[k][row]);
+        l = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0.f;
+#pragma unroll
+        for (int k = 0; k < kLanes; ++k) {
+            const float by = share_m[k][row] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(share_m[k][row] - m);
+            l += share_l[k][row] * by;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += share_v[k][row][d + i] * by;
         }
     }
     if (!live) return;
@@ -874,7 +885,7 @@ __global__ __launch_bounds__(256) void join(const AttnLaunch a)
     const int32_t tok = (int32_t)div_by(R, a.group_magic, a.group_shift);
     const int32_t head = gr.head * a.group + (int32_t)R - tok * a.group;
     store_out<T>(a, (int64_t)gr.q_begin + tok, head, d, v, l == 0.f ? 0.f : a.v_scale / l);
-    if (d == 0) store_lse(a, (int64_t)gr.q_begin + tok, head, top, l);
+    if (d == 0) store_lse(a, (int64_t)gr.q_begin + tok, head, m, l);
 }
 
 // ---- launches ---------------------------------------------------------------------

@@ -472,7 +472,7 @@ int kv_attend(kv_attn_plan *p, int32_t layer, const kv_attend_args *x, hipStream
     a.q_head = x->q_head_stride;
     a.out_token = x->out_token_stride;
     a.out_head = x->out_head_stride;
-    a.scale_log2 = (float)(x->softcap > 0 ? scale / x->softcap : scale * log2e);
+    a.scale_log2 = (float)((x->softcap > 0 ? 2 / (double)x->softcap : 1.0) * scale * log2e);
     a.cap_log2 = (float)(x->softcap * log2e);
     a.v_scale = e4m3 ? x->v_scale : 1.f;
     // a captured call holds every kernel that a plan within the limits may need

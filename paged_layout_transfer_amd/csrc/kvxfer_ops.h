@@ -148,7 +148,7 @@ struct AttnLaunch {
     float *lse;
     const float *slopes;
     int64_t q_token, q_head, out_token, out_head;  // elements
-    float scale_log2;     // scale * k_scale * log2(e), or scale * k_scale / softcap with a cap
+    float scale_log2;     // scale * k_scale * log2(e), times 2 / softcap with a cap
     float cap_log2;       // softcap * log2(e), or 0
     float k_scale, v_scale;
     const void *k_new, *v_new;

@@ -138,8 +138,8 @@ __device__ __forceinline__ float e4m3_of(float x, float scale)
 template <class T, bool E4M3>
 __global__ __launch_bounds__(kThreads) void append_tokens(const AttnLaunch a)
 {
-    if ((int32_t)blockIdx.x >= a.head->n_append) return;
     const AppendItem it = a.append[blockIdx.x];
+    if ((int32_t)blockIdx.x >= a.head->n_append) return;
     const uint32_t chunks = (uint32_t)a.dim / 8;               // of one head
     const uint32_t per_tok = chunks * (uint32_t)a.heads;
     const uint32_t total = per_tok * (uint32_t)it.count;

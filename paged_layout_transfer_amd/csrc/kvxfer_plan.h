@@ -24,10 +24,11 @@ struct PlanLimits {
 // Capacities that hold any plan of max_seqs sequences and max_tokens new tokens.  Of a class
 // with at most `pieces` pieces, split_class cuts at most cut_parts() parts, and makes at most all_parts()
 // parts in all.
-inline int64_t cut_parts(int64_t pieces, int64_t slots) { return pieces <= slots ? slots : 4 * slots; }
+inline int64_t max_rounds(int64_t pieces, int64_t slots) { return pieces <= slots ? 2 : 4; }
+inline int64_t cut_parts(int64_t pieces, int64_t slots) { return max_rounds(pieces, slots) * slots; }
 inline int64_t all_parts(int64_t pieces, int64_t slots)
 {
-    return pieces <= slots ? slots : std::max(4 * slots, pieces + 2 * slots);
+    return std::max(cut_parts(pieces, slots), pieces >= 4 * slots ? pieces + 2 * slots : 0);
 }
 
 inline PlanLimits plan_limits(const kv_pool_desc &d, const kv_attn_desc &a)
@@ -89,14 +90,14 @@ inline int64_t parts_at(const std::vector<AttnItem> &whole, int64_t share, int32
 }
 
 // When the last of `slots` workgroups ends, in tiles, if each takes the longest part left; a
-// part costs its tiles and one more for its start and end.  `ends` is scratch.
+// part costs its tiles and two more for its start and end.  `ends` is scratch.
 inline int64_t span_at(const std::vector<AttnItem> &whole, int64_t share, int64_t slots, std::vector<int64_t> &parts,
                        std::vector<int64_t> &ends)
 {
     parts.clear();
     for (const AttnItem &it : whole) {
         const int64_t n = std::max<int64_t>(1, (it.tile1 + share - 1) / share);
-        for (int64_t k = 0; k < n; ++k) parts.push_back(it.tile1 * (k + 1) / n - it.tile1 * k / n + 1);
+        for (int64_t k = 0; k < n; ++k) parts.push_back(it.tile1 * (k + 1) / n - it.tile1 * k / n + 2);
     }
     std::sort(parts.begin(), parts.end(), std::greater<int64_t>());
     ends.assign((size_t)slots, 0);  // a heap, the earliest end first
@@ -109,14 +110,13 @@ inline int64_t span_at(const std::vector<AttnItem> &whole, int64_t share, int64_
 }
 
 // Splits the pieces in `whole` (tile0 = 0, tile1 = all tiles, one for all cache heads) over the keys.
-//  * At most as many pieces as workgroups that run at once (slots): the smallest share of tiles
-//    whose parts do not outnumber them, so that all run in one go.
-//  * At least four times as many: only pieces longer than the even share are cut; the rest
-//    even out by themselves, longest first.
-//  * In between, where a last round of a few whole pieces would leave most of the chip idle:
-//    no cut, or the smallest share whose parts fill two, three or four rounds, whichever ends first.
-// At most 4 * slots parts in the first and last case; in the second a piece of t > share tiles
-// gives at most t / share + 1 < 2 t / share parts, and the sum of t / share is at most slots.
+//  * At least four times as many pieces as workgroups that run at once (slots): only pieces longer
+//    than the even share are cut; the rest even out by themselves, longest first.  A piece of t >
+//    share tiles gives at most t / share + 1 < 2 t / share parts, and the sum of t / share is at
+//    most slots.
+//  * Fewer: no cut, or the smallest share whose parts fill one, two, ... rounds, whichever
+//    ends first.  One round suits equal pieces; more even out unequal ones (32 sequences of 1 K to
+//    64 K tokens: one round 353 us, two 335 us, four 333 us; one sequence of 32 K: 34, 38, 49 us).
 // A part shorter than min_tiles is not worth its partial result's trip.
 inline void split_class(Plan &p, std::vector<AttnItem> &out, const PlanLimits &l, int32_t rows_of_piece,
                         int64_t slots, int64_t min_tiles, int64_t *prow)
@@ -127,8 +127,7 @@ inline void split_class(Plan &p, std::vector<AttnItem> &out, const PlanLimits &l
     const int64_t even = std::max(min_tiles, (total + slots - 1) / slots);
     const int64_t pieces = (int64_t)p.whole.size() * l.heads;
     auto fitting = [&](int64_t parts) {
-        int64_t lo = std::min(even, longest), hi = longest;
-        if (parts > slots) lo = std::min(min_tiles, longest);
+        int64_t lo = std::min(min_tiles, longest), hi = longest;
         while (lo < hi) {
             const int64_t mid = (lo + hi) / 2;
             if (parts_at(p.whole, mid, l.heads) <= parts) hi = mid;
@@ -137,14 +136,12 @@ inline void split_class(Plan &p, std::vector<AttnItem> &out, const PlanLimits &l
         return lo;
     };
     int64_t share = longest;
-    if (pieces <= slots) {
-        share = fitting(slots);
-    } else if (pieces >= 4 * slots) {
+    if (pieces >= 4 * slots) {
         share = std::min(even, longest);
     } else {
         const int64_t lanes = std::max<int64_t>(1, slots / l.heads);
         int64_t best = span_at(p.whole, longest, lanes, p.parts, p.ends);
-        for (int64_t rounds = 2; rounds <= 4; ++rounds) {
+        for (int64_t rounds = 1; rounds <= max_rounds(pieces, slots); ++rounds) {
             if (pieces > rounds * slots) continue;
             const int64_t s = fitting(rounds * slots), span = span_at(p.whole, s, lanes, p.parts, p.ends);
             // a split costs a trip through the workspace: only for a twentieth of the time
@@ -154,25 +151,27 @@ inline void split_class(Plan &p, std::vector<AttnItem> &out, const PlanLimits &l
     for (const AttnItem &it : p.whole) {
         const int64_t n = (it.tile1 + share - 1) / share;
         const int32_t rows = (int32_t)std::min<int64_t>(rows_of_piece, (int64_t)it.q_len * l.group - it.row0);
-        for (int32_t head = 0; head < l.heads; ++head) {
-            AttnItem part = it;
-            part.head = head;
-            if (n <= 1) {
-                out.push_back(part);
-                continue;
-            }
+        if (n <= 1) {
+            AttnItem whole = it;
+            for (whole.head = 0; whole.head < l.heads; ++whole.head) out.push_back(whole);
+            continue;
+        }
+        for (int32_t head = 0; head < l.heads; ++head)
             for (int32_t r = 0; r < rows; r += KVX_JOIN_ROWS)
-                p.groups.push_back(AttnGroup{(int32_t)*prow + r, (int32_t)n, rows_of_piece,
+                p.groups.push_back(AttnGroup{(int32_t)(*prow + head * n * rows_of_piece + r), (int32_t)n, rows_of_piece,
                                              std::min(KVX_JOIN_ROWS, rows - r), it.q_begin, it.q_len, head,
                                              it.row0 + r});
-            for (int64_t k = 0; k < n; ++k) {
+        // the heads of one stretch of keys side by side: they read neighbouring bytes of one page
+        for (int64_t k = 0; k < n; ++k)
+            for (int32_t head = 0; head < l.heads; ++head) {
+                AttnItem part = it;
+                part.head = head;
                 part.tile0 = (int32_t)(it.tile1 * k / n);
                 part.tile1 = (int32_t)(it.tile1 * (k + 1) / n);
-                part.prow = (int32_t)*prow;
-                *prow += rows_of_piece;
+                part.prow = (int32_t)(*prow + (head * n + k) * rows_of_piece);
                 out.push_back(part);
             }
-        }
+        *prow += l.heads * n * rows_of_piece;
     }
     // longest first, so that the last workgroups to start are the short ones
     std::stable_sort(out.begin(), out.end(), [](const AttnItem &a, const AttnItem &b) {
