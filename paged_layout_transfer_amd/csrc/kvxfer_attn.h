@@ -552,7 +552,7 @@ constexpr int many_lds() { return KVX_TILE_KEYS * (2 * (key_row<DP>() + value_ro
 // worked out an iteration before by one wave for all (a lane a key), and the block ids of tile i + 4
 // are fetched by another.  One barrier a tile.
 template <class T, bool E4M3, int DP, bool SHAPED>
-__global__ __launch_bounds__(64 * many_waves<DP>()) void attend_many(const AttnLaunch a)
+__global__ __launch_bounds__(64 * many_waves<DP>(), DP == 64 ? 4 : DP == 128 ? 2 : 1) void attend_many(const AttnLaunch a)
 {
     typedef typename Vec<T>::x8 T8;
     typedef typename Vec<T>::x4 T4;
