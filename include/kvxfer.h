@@ -456,7 +456,7 @@ KV_API int kv_scatter_chunks_dma(kv_pool *pool, const kv_span *spans, int32_t n_
  * KV_MAX_PAGE_COPIES) records.  Ids lie in [0, num_blocks) (KV_ERR_RANGE); no dst is named
  * twice or is the src of a record (KV_ERR_DUP): every byte has one writer and no byte that
  * is read is written.  Allocated or not is not looked at.  n == 0 is a no-op.  Returns after enqueueing.  Under
- * graph capture a call of at most 128 records is captured as its kernel once the pool has made a
+ * graph capture a call of at most 256 records is captured as its kernel once the pool has made a
  * call outside the capture; any other is refused with KV_ERR_CAPTURE.
  * No passage: the page maintenance next to the pages' transfers. */
 KV_API int kv_copy_pages(kv_pool *pool, const kv_page_copy *copies, int32_t n, int32_t layer_begin,

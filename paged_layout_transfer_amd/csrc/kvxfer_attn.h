@@ -31,6 +31,22 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 #define KVX_GLOBAL __attribute__((address_space(1)))
 #define KVX_LDS __attribute__((address_space(3)))
+#define KVX_CONST __attribute__((address_space(4)))
+
+// A plan record, the same for the whole workgroup and not written while kernels run: read
+// through the constant space, by scalar loads into scalar registers.
+template <class Rec>
+__device__ __forceinline__ Rec plan_record(const Rec *at)
+{
+    constexpr int kWords = sizeof(Rec) / 4;
+    union {
+        Rec rec;
+        uint32_t word[kWords];
+    } u;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) u.word[i] = ((const KVX_CONST uint32_t *)at)[i];
+    return u.rec;
+}
 
 template <class T>
 struct Vec {
@@ -313,8 +329,10 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_few(const AttnL
     __shared__ float join_m[4][16], join_l[4][16];
 
     // the record is read before the count is known: the array holds one for every workgroup
-    const AttnItem it = a.items[blockIdx.x];
-    if ((int32_t)blockIdx.x >= a.head->n_few) return;
+    const AttnItem it = plan_record(a.items + blockIdx.x);
+    const int32_t n_few = plan_record(a.head).n_few;
+    asm volatile("" : : "s"(it.kv_len), "s"(n_few));  // both on their way before either is waited for
+    if ((int32_t)blockIdx.x >= n_few) return;
     const Piece s = piece_of<16>(a, it);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int n = lane & 15, g = lane >> 4;
@@ -335,16 +353,24 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_few(const AttnL
     int32_t i = s.tile0 * 2 + wave;
     auto start = [&](int32_t i) { return s.walk.start(i >> 1) + (i & 1) * kStep; };
     auto key = [&](int32_t i, int t) { return seen_key(s, start(i) + 16 * t + n); };
-    auto load = [&](u32x4(&r)[2][kLoads], const uint8_t *base, const int64_t(&off)[2]) {
+    const bool whole_rows = a.dim == DP;
+    auto load = [&](u32x4(&r)[2][kLoads], const uint8_t *base, const int64_t(&off)[2]) __attribute__((always_inline)) {
+        if (whole_rows) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int c = 0; c < kLoads; ++c) {
-                r[t][c] = u32x4{0, 0, 0, 0};
-                if (DP == 128 && a.dim == DP) r[t][c] = *(const KVX_GLOBAL u32x4 *)(base + off[t] + c * 64 + g * 16);
-                else if (c * 4 * kVals + g * kVals < a.dim)
+                for (int c = 0; c < kLoads; ++c)
                     r[t][c] = *(const KVX_GLOBAL u32x4 *)(base + off[t] + c * 64 + g * 16);
-            }
+        } else {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int c = 0; c < kLoads; ++c) {
+                    r[t][c] = u32x4{0, 0, 0, 0};
+                    if (c * 4 * kVals + g * kVals < a.dim)
+                        r[t][c] = *(const KVX_GLOBAL u32x4 *)(base + off[t] + c * 64 + g * 16);
+                }
+        }
     };
     int64_t off[2] = {0, 0};
     int32_t blk[2] = {0, 0};
@@ -567,8 +593,8 @@ __global__ __launch_bounds__(64 * many_waves<DP>(), DP == 64 ? 4 : DP == 128 ? 2
     int64_t *const offs = (int64_t *)(values + 2 * N * kV);          // [4][N]
     __shared__ int32_t odd[2];  // one past the last tile (of either parity) with infinities or NaN in V
 
-    const AttnItem it = a.items[blockIdx.x];
-    if ((int32_t)blockIdx.x >= a.head->n_many) return;
+    const AttnItem it = plan_record(a.items + blockIdx.x);
+    if ((int32_t)blockIdx.x >= plan_record(a.head).n_many) return;
     const Piece s = piece_of<32 * kWaves>(a, it);
     const int32_t n_tiles = s.tile1 - s.tile0;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -839,8 +865,8 @@ __global__ __launch_bounds__(256) void join(const AttnLaunch a)
     static_assert(kLanes >= 1, "");
     __shared__ float share_m[kLanes][KVX_JOIN_ROWS], share_l[kLanes][KVX_JOIN_ROWS];
     __shared__ __attribute__((aligned(16))) float share_v[kLanes][KVX_JOIN_ROWS][DP];
-    const AttnGroup gr = a.groups[blockIdx.x];
-    if ((int32_t)blockIdx.x >= a.head->n_groups) return;
+    const AttnGroup gr = plan_record(a.groups + blockIdx.x);
+    if ((int32_t)blockIdx.x >= plan_record(a.head).n_groups) return;
     const int d = threadIdx.x % kCols * 8, row = threadIdx.x / kCols % KVX_JOIN_ROWS;
     const int k0 = threadIdx.x / (kCols * KVX_JOIN_ROWS);
     const bool live = row < gr.rows;

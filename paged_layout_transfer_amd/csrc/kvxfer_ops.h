@@ -17,7 +17,7 @@ namespace kvx {
 
 // ---- pages -------------------------------------------------------------------
 
-#define KVX_INLINE_COPIES 128  // records that ride in the kernel arguments (1.5 KiB)
+#define KVX_INLINE_COPIES 256  // records that ride in the kernel arguments (3 KiB)
 #define KVX_COPY_PART 8192     // bytes of a page one wave copies
 
 struct CopyLaunch {
@@ -53,7 +53,7 @@ int launch_remap(const RemapLaunch &a, hipStream_t stream);
 
 #define KVX_TILE_KEYS 64      // keys of one tile: the unit in which work is counted and split
 #define KVX_ROWS_FEW 16       // rows of a piece of the few-rows kernel
-#define KVX_APPEND_TOKENS 16  // new tokens of one append item
+#define KVX_APPEND_TOKENS 8   // new tokens of one append item
 #define KVX_JOIN_ROWS 4       // rows joined by one workgroup
 
 // Rows of a piece of the many-rows kernel: 32 to a wave; at the widest heads a wave's

@@ -134,49 +134,68 @@ __device__ __forceinline__ float e4m3_of(float x, float scale)
     return y != y ? y : fminf(fmaxf(y, -448.f), 448.f);
 }
 
-// One workgroup writes one item's tokens, keys then values: 8 elements a thread.
+// One workgroup writes one item's tokens.  A thread owns eight values of a token's row (of its
+// keys, then its values) and goes over the tokens, four at a time: their block ids, then their rows,
+// then the stores.  Bound by the latency of that chain for a decode step's tokens, by HBM for a chunk's.
 template <class T, bool E4M3>
 __global__ __launch_bounds__(kThreads) void append_tokens(const AttnLaunch a)
 {
+    typedef T T8 __attribute__((ext_vector_type(8)));
+    constexpr int kBatch = 4;
     const AppendItem it = a.append[blockIdx.x];
     if ((int32_t)blockIdx.x >= a.head->n_append) return;
-    const uint32_t chunks = (uint32_t)a.dim / 8;               // of one head
+    const uint32_t chunks = (uint32_t)a.dim / 8;  // of one head
     const uint32_t per_tok = chunks * (uint32_t)a.heads;
-    const uint32_t total = per_tok * (uint32_t)it.count;
-    for (uint32_t i = threadIdx.x; i < 2 * total; i += kThreads) {
-        const bool val = i >= total;
-        const uint32_t c = val ? i - total : i;
-        const uint32_t t = c / per_tok, hc = c - t * per_tok, h = hc / chunks, e = hc - h * chunks;
-        const int64_t row = (int64_t)it.row + t;
-        if (row >= a.n_tokens) continue;
-        const uint32_t pos = (uint32_t)it.pos + t;
-        const uint32_t page = div_by(pos, a.bs_magic, a.bs_shift), slot = pos - page * a.block_size;
-        const int32_t blk = it.table[page];
-        if ((uint32_t)blk >= a.num_blocks) {
-            if (hc == 0) atomicOr(a.err, KV_DEVERR_BLOCK_RANGE);
-            continue;
-        }
-        const T *src = (val ? (const T *)a.v_new + row * a.v_token + (int64_t)h * a.v_head
-                            : (const T *)a.k_new + row * a.k_token + (int64_t)h * a.k_head) + e * 8;
-        uint8_t *dst = (val ? a.v_base : a.k_base) + (int64_t)blk * a.block_stride +
-                       (int64_t)slot * a.tok_stride + (int64_t)h * a.head_stride;
-        typedef T T8 __attribute__((ext_vector_type(8)));
-        const T8 x = *(const T8 *)src;
-        if (!E4M3) {
-            *(T8 *)(dst + e * 16) = x;
-        } else {
-            const float sc = val ? a.v_scale : a.k_scale;
-            uint32_t w[2];
+    const uint32_t lanes = min(2 * per_tok, (uint32_t)kThreads), at_once = kThreads / lanes;
+    const uint32_t t0 = threadIdx.x / lanes;
+    if (t0 >= at_once) return;
+    for (uint32_t c = threadIdx.x - t0 * lanes; c < 2 * per_tok; c += lanes) {
+        const bool val = c >= per_tok;
+        const uint32_t hc = val ? c - per_tok : c, h = hc / chunks, e = hc - h * chunks;
+        const T *src = (val ? (const T *)a.v_new + (int64_t)h * a.v_head : (const T *)a.k_new + (int64_t)h * a.k_head) + e * 8;
+        const int64_t src_tok = val ? a.v_token : a.k_token;
+        uint8_t *dst = (val ? a.v_base : a.k_base) + (int64_t)h * a.head_stride + e * (E4M3 ? 8 : 16);
+        const float scale = val ? a.v_scale : a.k_scale;
+        for (uint32_t t = t0; t < (uint32_t)it.count; t += kBatch * at_once) {
+            int32_t blk[kBatch];
+            T8 x[kBatch];
+            bool ok[kBatch];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                int p = 0;
-                p = __builtin_amdgcn_cvt_pk_fp8_f32(e4m3_of((float)x[4 * k], sc), e4m3_of((float)x[4 * k + 1], sc), p,
-                                                    false);
-                p = __builtin_amdgcn_cvt_pk_fp8_f32(e4m3_of((float)x[4 * k + 2], sc),
-                                                    e4m3_of((float)x[4 * k + 3], sc), p, true);
-                w[k] = (uint32_t)p;
+            for (int u = 0; u < kBatch; ++u) {
+                const uint32_t tt = t + u * at_once;
+                ok[u] = tt < (uint32_t)it.count && (int64_t)it.row + tt < a.n_tokens;
+                blk[u] = 0;
+                if (ok[u]) {
+                    blk[u] = it.table[div_by((uint32_t)it.pos + tt, a.bs_magic, a.bs_shift)];
+                    x[u] = *(const T8 *)(src + ((int64_t)it.row + tt) * src_tok);
+                }
             }
-            *(uint2 *)(dst + e * 8) = make_uint2(w[0], w[1]);
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                if (!ok[u]) continue;
+                const uint32_t pos = (uint32_t)it.pos + t + u * at_once;
+                const uint32_t slot = pos - div_by(pos, a.bs_magic, a.bs_shift) * a.block_size;
+                if ((uint32_t)blk[u] >= a.num_blocks) {
+                    if (c == 0) atomicOr(a.err, KV_DEVERR_BLOCK_RANGE);
+                    continue;
+                }
+                uint8_t *to = dst + (int64_t)blk[u] * a.block_stride + (int64_t)slot * a.tok_stride;
+                if (!E4M3) {
+                    *(T8 *)to = x[u];
+                    continue;
+                }
+                uint32_t w[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    int p = 0;
+                    p = __builtin_amdgcn_cvt_pk_fp8_f32(e4m3_of((float)x[u][4 * k], scale),
+                                                        e4m3_of((float)x[u][4 * k + 1], scale), p, false);
+                    p = __builtin_amdgcn_cvt_pk_fp8_f32(e4m3_of((float)x[u][4 * k + 2], scale),
+                                                        e4m3_of((float)x[u][4 * k + 3], scale), p, true);
+                    w[k] = (uint32_t)p;
+                }
+                *(uint2 *)to = make_uint2(w[0], w[1]);
+            }
         }
     }
 }

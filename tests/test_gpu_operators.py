@@ -560,7 +560,7 @@ def test_page_copies(head_major, heads, dim, kind, n):
         assert torch.equal(c.dev.cpu(), want)
 
 
-@pytest.mark.parametrize("n", [0, 1, 128, 129, 4096, 5000])
+@pytest.mark.parametrize("n", [0, 1, 256, 257, 4096, 5000])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_remapped_tables(n, in_place):
     rng = np.random.default_rng(n)
@@ -583,9 +583,9 @@ def test_remapped_tables(n, in_place):
 
 
 def test_copies_and_remaps_captured():
-    with Cache(heads=2, dim=64, page=16, blocks=400, kind="bf16") as c:
+    with Cache(heads=2, dim=64, page=16, blocks=600, kind="bf16") as c:
         few = K.make_page_copies([(i, 200 + i, 16 - i % 3) for i in range(100)])
-        lots = K.make_page_copies([(i, 200 + i, 16) for i in range(150)])
+        lots = K.make_page_copies([(i, 300 + i, 16) for i in range(257)])
         t = torch.arange(400, dtype=torch.int32, device="cuda")
         out = torch.zeros_like(t)
         side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
