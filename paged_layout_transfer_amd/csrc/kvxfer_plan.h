@@ -89,15 +89,27 @@ inline int64_t parts_at(const std::vector<AttnItem> &whole, int64_t share, int32
     return n * heads;
 }
 
-// When the last of `slots` workgroups ends, in tiles, if each takes the longest part left; a
-// part costs its tiles and two more for its start and end.  `ends` is scratch.
-inline int64_t span_at(const std::vector<AttnItem> &whole, int64_t share, int64_t slots, std::vector<int64_t> &parts,
-                       std::vector<int64_t> &ends)
+// What splitting costs, in the time of one tile: a part's start and end, whole or cut, and the join.
+// Many rows: a cut part writes 128 KiB that the join reads, about three tiles each way at a
+// compute unit's share of HBM.  Few rows: a part's 8 KiB are nothing, but the join's launch takes 4 us,
+// ten tiles of a workgroup.
+struct SplitCost {
+    int64_t whole, cut, join, min_tiles;
+};
+constexpr SplitCost kCostFew{2, 2, 10, 2}, kCostMany{1, 6, 2, 8};
+
+// When the last of `slots` workgroups ends, in tiles, if each takes the longest part left.
+// `ends` is scratch.
+inline int64_t span_at(const std::vector<AttnItem> &whole, int64_t share, int64_t slots, const SplitCost &cost,
+                       std::vector<int64_t> &parts, std::vector<int64_t> &ends)
 {
     parts.clear();
+    bool any = false;
     for (const AttnItem &it : whole) {
         const int64_t n = std::max<int64_t>(1, (it.tile1 + share - 1) / share);
-        for (int64_t k = 0; k < n; ++k) parts.push_back(it.tile1 * (k + 1) / n - it.tile1 * k / n + 2);
+        any |= n > 1;
+        for (int64_t k = 0; k < n; ++k)
+            parts.push_back(it.tile1 * (k + 1) / n - it.tile1 * k / n + (n > 1 ? cost.cut : cost.whole));
     }
     std::sort(parts.begin(), parts.end(), std::greater<int64_t>());
     ends.assign((size_t)slots, 0);  // a heap, the earliest end first
@@ -106,7 +118,7 @@ inline int64_t span_at(const std::vector<AttnItem> &whole, int64_t share, int64_
         ends.back() += p;
         std::push_heap(ends.begin(), ends.end(), std::greater<int64_t>());
     }
-    return *std::max_element(ends.begin(), ends.end());
+    return *std::max_element(ends.begin(), ends.end()) + (any ? cost.join : 0);
 }
 
 // Splits the pieces in `whole` (tile0 = 0, tile1 = all tiles, one for all cache heads) over the keys.
@@ -114,20 +126,20 @@ inline int64_t span_at(const std::vector<AttnItem> &whole, int64_t share, int64_
 //    than the even share are cut; the rest even out by themselves, longest first.  A piece of t >
 //    share tiles gives at most t / share + 1 < 2 t / share parts, and the sum of t / share is at
 //    most slots.
-//  * Fewer: no cut, or the smallest share whose parts fill one, two, ... rounds, whichever
-//    ends first.  One round suits equal pieces; more even out unequal ones (32 sequences of 1 K to
+//  * Fewer: no cut, the smallest share whose parts fill one, two, ... rounds, or the longest piece
+//    cut in two, three or four and the others where they are longer, whichever ends first.  One round suits equal pieces; more even out unequal ones (32 sequences of 1 K to
 //    64 K tokens: one round 353 us, two 335 us, four 333 us; one sequence of 32 K: 34, 38, 49 us).
-// A part shorter than min_tiles is not worth its partial result's trip.
+// Without the costs of a cut, a prompt of 2048 tokens was cut into parts of 11 tiles and took 68 us.
 inline void split_class(Plan &p, std::vector<AttnItem> &out, const PlanLimits &l, int32_t rows_of_piece,
-                        int64_t slots, int64_t min_tiles, int64_t *prow)
+                        int64_t slots, const SplitCost &cost, int64_t *prow)
 {
     int64_t total = 0, longest = 1;
     for (const AttnItem &it : p.whole)
         total += (int64_t)it.tile1 * l.heads, longest = std::max<int64_t>(longest, it.tile1);
-    const int64_t even = std::max(min_tiles, (total + slots - 1) / slots);
+    const int64_t even = std::max(cost.min_tiles, (total + slots - 1) / slots);
     const int64_t pieces = (int64_t)p.whole.size() * l.heads;
     auto fitting = [&](int64_t parts) {
-        int64_t lo = std::min(min_tiles, longest), hi = longest;
+        int64_t lo = std::min(cost.min_tiles, longest), hi = longest;
         while (lo < hi) {
             const int64_t mid = (lo + hi) / 2;
             if (parts_at(p.whole, mid, l.heads) <= parts) hi = mid;
@@ -140,13 +152,15 @@ inline void split_class(Plan &p, std::vector<AttnItem> &out, const PlanLimits &l
         share = std::min(even, longest);
     } else {
         const int64_t lanes = std::max<int64_t>(1, slots / l.heads);
-        int64_t best = span_at(p.whole, longest, lanes, p.parts, p.ends);
-        for (int64_t rounds = 1; rounds <= max_rounds(pieces, slots); ++rounds) {
-            if (pieces > rounds * slots) continue;
-            const int64_t s = fitting(rounds * slots), span = span_at(p.whole, s, lanes, p.parts, p.ends);
-            // a split costs a trip through the workspace: only for a twentieth of the time
-            if (span * 20 < best * 19) best = span, share = s;
-        }
+        int64_t best = span_at(p.whole, longest, lanes, cost, p.parts, p.ends);
+        auto consider = [&](int64_t s) {
+            if (s >= longest || parts_at(p.whole, s, l.heads) > max_rounds(pieces, slots) * slots) return;
+            const int64_t span = span_at(p.whole, s, lanes, cost, p.parts, p.ends);
+            if (span < best) best = span, share = s;
+        };
+        for (int64_t rounds = 1; rounds <= max_rounds(pieces, slots); ++rounds)
+            if (pieces <= rounds * slots) consider(fitting(rounds * slots));
+        for (int64_t cuts = 2; cuts <= 4; ++cuts) consider(std::max(cost.min_tiles, (longest + cuts - 1) / cuts));
     }
     for (const AttnItem &it : p.whole) {
         const int64_t n = (it.tile1 + share - 1) / share;
@@ -215,7 +229,7 @@ inline void build_plan(Plan &p, const PlanLimits &l, const kv_seq *seqs, int32_t
                 p.whole.push_back(it);
             }
         }
-        split_class(p, few ? p.few : p.many, l, step, few ? l.slots_few : kSlotsMany, few ? 2 : 4, &prow);
+        split_class(p, few ? p.few : p.many, l, step, few ? l.slots_few : kSlotsMany, few ? kCostFew : kCostMany, &prow);
     }
     for (int32_t i = 0; i < n; ++i) {
         const kv_seq &s = seqs[i];
