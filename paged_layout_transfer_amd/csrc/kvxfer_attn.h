@@ -308,8 +308,9 @@ __device__ __forceinline__ void store_lse(const AttnLaunch &a, int64_t row, int3
 
 // ---- few rows: single tokens and drafts ----------------------------------------
 
-// At most 16 rows (16x16x32 products).  Four waves take the piece's 32-key steps in turn,
-// each with its own running maximum, and join at the end in shared memory.  Bound by the
+// At most 16 rows (16x16x32 products).  Four waves take the piece's 32-key steps in turn, each
+// with its own running maximum, and join at the end in shared memory; or each takes a cache head
+// (AttnItem::across).  Bound by the
 // cache's bytes: keys go from memory to the first product's registers directly, values through a
 // slice of shared memory of the wave's own, both loaded a step ahead and their block ids two, with
 // no barrier in the loop.
@@ -333,8 +334,14 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_few(const AttnL
     const int32_t n_few = plan_record(a.head).n_few;
     asm volatile("" : : "s"(it.kv_len), "s"(n_few));  // both on their way before either is waited for
     if ((int32_t)blockIdx.x >= n_few) return;
-    const Piece s = piece_of<16>(a, it);
+    Piece s = piece_of<16>(a, it);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const bool across = it.across != 0;
+    if (across) {
+        s.head += wave;
+        if (s.prow >= 0) s.prow += 16 * wave;
+    }
+    const int32_t first = across ? 0 : wave, apart = across ? 1 : 4;  // the wave's steps
     const int n = lane & 15, g = lane >> 4;
     T *tile = (T *)(shared + wave * kSlice);
 
@@ -350,7 +357,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_few(const AttnL
 
     u32x4 kr[2][kLoads], vr[2][kLoads];
     const int32_t i1 = s.tile1 * 2;
-    int32_t i = s.tile0 * 2 + wave;
+    int32_t i = s.tile0 * 2 + first;
     auto start = [&](int32_t i) { return s.walk.start(i >> 1) + (i & 1) * kStep; };
     auto key = [&](int32_t i, int t) { return seen_key(s, start(i) + 16 * t + n); };
     const bool whole_rows = a.dim == DP;
@@ -382,9 +389,9 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_few(const AttnL
         load(kr, a.k_base, off);
         load(vr, a.v_base, off);
     }
-    if (i + 4 < i1) {
+    if (i + apart < i1) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) blk[t] = block_of(a, s, key(i + 4, t));
+        for (int t = 0; t < 2; ++t) blk[t] = block_of(a, s, key(i + apart, t));
     }
     T8 q[kS];
     const T *qr = q_row<T>(a, s, n);
@@ -398,12 +405,12 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_few(const AttnL
     const float sc = SHAPED ? 1.f : a.scale_log2;
     const float slack = 8.f / sc;  // a maximum that grows by less than 2^8 is not worth a rescaling
 
-    for (; i < i1; i += 4) {
+    for (; i < i1; i += apart) {
         const int32_t j0 = start(i);
-        const bool more = i + 4 < i1;
+        const bool more = i + apart < i1;
         if (more) {
 #pragma unroll
-            for (int t = 0; t < 2; ++t) off[t] = key_offset(a, s, key(i + 4, t), blk[t]);
+            for (int t = 0; t < 2; ++t) off[t] = key_offset(a, s, key(i + apart, t), blk[t]);
         }
         // S^T: keys 16 t + 4 g + r of the step against row n
         f32x4 x[2];
@@ -439,9 +446,9 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_few(const AttnL
                 }
             }
         if (more) load(vr, a.v_base, off);
-        if (i + 8 < i1) {
+        if (i + 2 * apart < i1) {
 #pragma unroll
-            for (int t = 0; t < 2; ++t) blk[t] = block_of(a, s, key(i + 8, t));
+            for (int t = 0; t < 2; ++t) blk[t] = block_of(a, s, key(i + 2 * apart, t));
         }
         // the slice is the wave's own and its accesses stay in order: no barrier, but the
         // compiler must not move the reads below above the writes of other lanes
@@ -514,19 +521,22 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_few(const AttnL
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
 
-    // join the four waves: their slices hold 16 rows of 32-bit results
-    __syncthreads();
-    float *part = (float *)tile;
-    if (g == 0) join_m[wave][n] = m == -INFINITY ? m : m * sc, join_l[wave][n] = l;
-    __syncthreads();
-    float top = -INFINITY;
+    // join the four waves: their slices hold 16 rows of 32-bit results.  With a head to each wave
+    // there is nothing to join, and a wave reads its own slice back, a row at a time.
+    const float mine = m == -INFINITY ? m : m * sc;
+    if (g == 0) join_m[wave][n] = mine, join_l[wave][n] = l;
+    __syncthreads();  // the slices' values are no longer needed
+    float top = mine;
+    if (!across) {
 #pragma unroll
-    for (int w = 0; w < 4; ++w) top = fmaxf(top, join_m[w][n]);
-    const float by = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m * sc - top);
+        for (int w = 0; w < 4; ++w) top = fmaxf(top, join_m[w][n]);
+    }
+    const float by = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mine - top);
 #pragma unroll
-    for (int d = 0; d < DP / 16; ++d) *(f32x4 *)(part + n * DP + d * 16 + 4 * g) = o[d] * by;
+    for (int d = 0; d < DP / 16; ++d) *(f32x4 *)((float *)tile + n * DP + d * 16 + 4 * g) = o[d] * by;
     __syncthreads();
-    const int row = threadIdx.x >> 4;
+    const int at = across ? lane : (int)threadIdx.x, wide = across ? 4 : 16;  // threads of a row
+    const int row = at / wide, w0 = across ? wave : 0, w1 = across ? wave + 1 : 4;
     if (row >= s.rows) return;
     const uint32_t Rr = (uint32_t)(s.row0 + row);
     const int32_t t_r = (int32_t)div_by(Rr, a.group_magic, a.group_shift);
@@ -534,15 +544,12 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_few(const AttnL
     const int64_t to_row = (int64_t)s.q_begin + t_r;
     float sum = 0.f;
     top = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) top = fmaxf(top, join_m[w][row]);
-#pragma unroll
-    for (int w = 0; w < 4; ++w)
+    for (int w = w0; w < w1; ++w) top = fmaxf(top, join_m[w][row]);
+    for (int w = w0; w < w1; ++w)
         if (join_m[w][row] != -INFINITY) sum += join_l[w][row] * __builtin_amdgcn_exp2f(join_m[w][row] - top);
-    for (int d = (threadIdx.x & 15) * 8; d < DP; d += 128) {
+    for (int d = at % wide * 8; d < DP; d += wide * 8) {
         float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll
-        for (int w = 0; w < 4; ++w)
+        for (int w = w0; w < w1; ++w)
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] += ((float *)(shared + w * kSlice))[row * DP + d + k];
         if (s.prow >= 0) {
@@ -553,7 +560,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_few(const AttnL
             store_out<T>(a, to_row, head, d, v, sum == 0.f ? 0.f : a.v_scale / sum);
         }
     }
-    if ((threadIdx.x & 15) == 0) {
+    if (at % wide == 0) {
         if (s.prow >= 0) {
             a.part_ml[2 * ((int64_t)s.prow + row)] = top;
             a.part_ml[2 * ((int64_t)s.prow + row) + 1] = sum;

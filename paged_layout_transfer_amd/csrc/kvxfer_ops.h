@@ -53,6 +53,12 @@ int launch_remap(const RemapLaunch &a, hipStream_t stream);
 
 #define KVX_TILE_KEYS 64      // keys of one tile: the unit in which work is counted and split
 #define KVX_ROWS_FEW 16       // rows of a piece of the few-rows kernel
+// Tiles, all heads counted, to each workgroup that runs at once from which a workgroup's waves take a head
+// each (token-major pages).  A wave's 256-byte rows of one head lie heads * 256 bytes apart; four waves on
+// neighbouring heads read 1 KiB runs: 64 sequences of 8 K tokens 392 -> 364 us, as head-major pages
+// (356 us).  Below it there are more parts to join than this gains: one sequence of 32 K (8
+// tiles) 35 -> 42 us, sixteen of 200 to 5015 (10 tiles) 222 -> 213 us for four layers.
+#define KVX_ACROSS 10
 #define KVX_APPEND_TOKENS 8   // new tokens of one append item
 #define KVX_JOIN_ROWS 4       // rows joined by one workgroup
 
@@ -67,8 +73,9 @@ struct AttnItem {
     const int32_t *table;
     int32_t kv_len, q_begin, q_len, prefix;
     int32_t head, row0, tile0, tile1;
-    int32_t prow;  // first row in the workspace of partial results, or -1: the result is whole
-    int32_t pad;
+    int32_t prow;    // first row in the workspace of partial results, or -1: the result is whole
+    int32_t across;  // few rows: the four waves take the cache heads head .. head + 3 instead of
+                     // every fourth step of one head; wave w's partial rows lie 16 w behind prow
 };
 static_assert(sizeof(AttnItem) == 48, "");
 

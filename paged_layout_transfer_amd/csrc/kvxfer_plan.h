@@ -17,7 +17,7 @@ constexpr int32_t kSlotsMany = 256;
 
 struct PlanLimits {
     int32_t heads, group, window, rows_many, slots_few;
-    bool full;
+    bool full, token_major;
     int64_t cap_few, cap_many, cap_groups, cap_append, cap_prows;
 };
 
@@ -38,6 +38,7 @@ inline PlanLimits plan_limits(const kv_pool_desc &d, const kv_attn_desc &a)
     l.group = a.num_q_heads / d.num_heads;
     l.window = a.window;
     l.full = (a.flags & KV_ATTN_FULL) != 0;
+    l.token_major = d.page_layout == KV_PAGE_TOKEN_MAJOR;
     l.rows_many = rows_many(d.head_dim);
     l.slots_few = slots_few(d.head_dim);
     const int64_t rows = a.max_tokens * l.group;
@@ -46,7 +47,8 @@ inline PlanLimits plan_limits(const kv_pool_desc &d, const kv_attn_desc &a)
     const int64_t few = seqs * l.heads, cut_few = cut_parts(few, l.slots_few);
     l.cap_few = all_parts(few, l.slots_few);
     l.cap_groups = cut_few / 2 * slices(std::min<int64_t>(rows, KVX_ROWS_FEW));
-    l.cap_prows = cut_few * KVX_ROWS_FEW;
+    l.cap_prows = cut_few * KVX_ROWS_FEW * (l.heads % 4 == 0 ? 4 : 1);
+    l.cap_groups *= l.heads % 4 == 0 ? 4 : 1;
     l.cap_many = 0;
     if (rows > KVX_ROWS_FEW) {
         const int64_t many = (rows / l.rows_many + seqs) * l.heads, cut_many = cut_parts(many, kSlotsMany);
@@ -131,18 +133,23 @@ inline int64_t span_at(const std::vector<AttnItem> &whole, int64_t share, int64_
 //    64 K tokens: one round 353 us, two 335 us, four 333 us; one sequence of 32 K: 34, 38, 49 us).
 // Without the costs of a cut, a prompt of 2048 tokens was cut into parts of 11 tiles and took 68 us.
 inline void split_class(Plan &p, std::vector<AttnItem> &out, const PlanLimits &l, int32_t rows_of_piece,
-                        int64_t slots, const SplitCost &cost, int64_t *prow)
+                        int64_t slots, const SplitCost &cost, bool few, int64_t *prow)
 {
     int64_t total = 0, longest = 1;
     for (const AttnItem &it : p.whole)
         total += (int64_t)it.tile1 * l.heads, longest = std::max<int64_t>(longest, it.tile1);
+    // Four heads to a workgroup where they are neighbours in a page and there is work enough to
+    // give every wave some steps of its head.
+    const int32_t across = few && l.token_major && l.heads % 4 == 0 && total >= KVX_ACROSS * slots ? 4 : 1;
+    const int32_t units = l.heads / across;
+    total /= across;
     const int64_t even = std::max(cost.min_tiles, (total + slots - 1) / slots);
-    const int64_t pieces = (int64_t)p.whole.size() * l.heads;
+    const int64_t pieces = (int64_t)p.whole.size() * units;
     auto fitting = [&](int64_t parts) {
         int64_t lo = std::min(cost.min_tiles, longest), hi = longest;
         while (lo < hi) {
             const int64_t mid = (lo + hi) / 2;
-            if (parts_at(p.whole, mid, l.heads) <= parts) hi = mid;
+            if (parts_at(p.whole, mid, units) <= parts) hi = mid;
             else lo = mid + 1;
         }
         return lo;
@@ -151,10 +158,10 @@ inline void split_class(Plan &p, std::vector<AttnItem> &out, const PlanLimits &l
     if (pieces >= 4 * slots) {
         share = std::min(even, longest);
     } else {
-        const int64_t lanes = std::max<int64_t>(1, slots / l.heads);
+        const int64_t lanes = std::max<int64_t>(1, slots / units);
         int64_t best = span_at(p.whole, longest, lanes, cost, p.parts, p.ends);
         auto consider = [&](int64_t s) {
-            if (s >= longest || parts_at(p.whole, s, l.heads) > max_rounds(pieces, slots) * slots) return;
+            if (s >= longest || parts_at(p.whole, s, units) > max_rounds(pieces, slots) * slots) return;
             const int64_t span = span_at(p.whole, s, lanes, cost, p.parts, p.ends);
             if (span < best) best = span, share = s;
         };
@@ -165,27 +172,29 @@ inline void split_class(Plan &p, std::vector<AttnItem> &out, const PlanLimits &l
     for (const AttnItem &it : p.whole) {
         const int64_t n = (it.tile1 + share - 1) / share;
         const int32_t rows = (int32_t)std::min<int64_t>(rows_of_piece, (int64_t)it.q_len * l.group - it.row0);
+        AttnItem part = it;
+        part.across = across > 1;
         if (n <= 1) {
-            AttnItem whole = it;
-            for (whole.head = 0; whole.head < l.heads; ++whole.head) out.push_back(whole);
+            for (part.head = 0; part.head < l.heads; part.head += across) out.push_back(part);
             continue;
         }
+        // part k of head h at prow + (h / across * n + k) * stride + h mod across * 16
+        const int32_t stride = rows_of_piece * across;
         for (int32_t head = 0; head < l.heads; ++head)
             for (int32_t r = 0; r < rows; r += KVX_JOIN_ROWS)
-                p.groups.push_back(AttnGroup{(int32_t)(*prow + head * n * rows_of_piece + r), (int32_t)n, rows_of_piece,
-                                             std::min(KVX_JOIN_ROWS, rows - r), it.q_begin, it.q_len, head,
-                                             it.row0 + r});
+                p.groups.push_back(AttnGroup{
+                    (int32_t)(*prow + head / across * n * stride + head % across * rows_of_piece + r), (int32_t)n,
+                    stride, std::min(KVX_JOIN_ROWS, rows - r), it.q_begin, it.q_len, head, it.row0 + r});
         // the heads of one stretch of keys side by side: they read neighbouring bytes of one page
         for (int64_t k = 0; k < n; ++k)
-            for (int32_t head = 0; head < l.heads; ++head) {
-                AttnItem part = it;
+            for (int32_t head = 0; head < l.heads; head += across) {
                 part.head = head;
                 part.tile0 = (int32_t)(it.tile1 * k / n);
                 part.tile1 = (int32_t)(it.tile1 * (k + 1) / n);
-                part.prow = (int32_t)(*prow + (head * n + k) * rows_of_piece);
+                part.prow = (int32_t)(*prow + (head / across * n + k) * stride);
                 out.push_back(part);
             }
-        *prow += l.heads * n * rows_of_piece;
+        *prow += units * n * stride;
     }
     // longest first, so that the last workgroups to start are the short ones
     std::stable_sort(out.begin(), out.end(), [](const AttnItem &a, const AttnItem &b) {
@@ -229,7 +238,7 @@ inline void build_plan(Plan &p, const PlanLimits &l, const kv_seq *seqs, int32_t
                 p.whole.push_back(it);
             }
         }
-        split_class(p, few ? p.few : p.many, l, step, few ? l.slots_few : kSlotsMany, few ? kCostFew : kCostMany, &prow);
+        split_class(p, few ? p.few : p.many, l, step, few ? l.slots_few : kSlotsMany, few ? kCostFew : kCostMany, few, &prow);
     }
     for (int32_t i = 0; i < n; ++i) {
         const kv_seq &s = seqs[i];

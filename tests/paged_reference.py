@@ -19,10 +19,11 @@ def paged(region: torch.Tensor, head_major: bool) -> torch.Tensor:
 
 def cache_of(region, head_major, table, n):
     """The first n cached tokens of a sequence, [n][heads][dim] in 64 bits."""
-    view = paged(region.to(torch.float32).double(), head_major)
+    bits = region.view(torch.uint8 if region.element_size() == 1 else torch.int16)
+    view = paged(bits, head_major)
     bs = view.shape[1]
     j = torch.arange(n)
-    return view[table.long()[j // bs], j % bs]
+    return view[table.long()[j // bs], j % bs].contiguous().view(region.dtype).to(torch.float32).double()
 
 
 def visible(q_len, kv_len, window=0, prefix=0, full=False):

@@ -44,7 +44,8 @@ int main()
     }
     for (int round = 0; round < 120; ++round) {
         kv_pool_desc d{};
-        d.num_heads = 1 + (int32_t)below(3);
+        d.num_heads = below(3) ? 1 + (int32_t)below(3) : 4;
+        d.page_layout = below(3) ? KV_PAGE_TOKEN_MAJOR : KV_PAGE_HEAD_MAJOR;
         d.block_size = 16;
         kv_attn_desc a{};
         d.head_dim = below(2) ? 64 : 256;
@@ -61,6 +62,7 @@ int main()
             s.q_len = (int32_t)(below(3) ? below(4) : below(60));
             s.kv_len = below(5) ? s.q_len + below(500) : below(40);  // some shorter than their queries
             if (below(8) == 0) s.kv_len += 9000;
+            if (round % 20 == 0 && i == 0) s.kv_len = 180000, s.q_len = 1, s.prefix_len = 0;  // work for a head a wave
             s.prefix_len = below(2) ? 0 : (int32_t)below(700);
             s.q_begin = at;
             at += s.q_len;
@@ -77,7 +79,12 @@ int main()
         std::map<std::tuple<const int32_t *, int, int64_t>, std::vector<uint8_t>> walked;
         std::map<int32_t, std::tuple<int32_t, int32_t, int32_t>> parts;  // prow -> (q_begin, head, row0)
         for (int cls = 0; cls < 2; ++cls)
-            for (const AttnItem &it : cls ? p.many : p.few) {
+            for (const AttnItem &whole : cls ? p.many : p.few)
+            for (int wave = 0; wave < (whole.across ? 4 : 1); ++wave) {  // a head to each wave
+                AttnItem it = whole;
+                CHECK(!whole.across || !cls);
+                it.head += wave;
+                if (it.prow >= 0) it.prow += 16 * wave;
                 const int step = cls ? l.rows_many : KVX_ROWS_FEW;
                 CHECK(it.head >= 0 && it.head < d.num_heads && it.row0 % step == 0);
                 const int64_t rows = std::min<int64_t>(step, (int64_t)it.q_len * l.group - it.row0);
@@ -123,10 +130,10 @@ int main()
             }
         for (int cls = 0; cls < 2; ++cls)
             for (const AttnItem &it : cls ? p.many : p.few)
-                if (it.prow >= 0) {
+                for (int wave = 0; it.prow >= 0 && wave < (it.across ? 4 : 1); ++wave) {
                     const int64_t rows = std::min<int64_t>(cls ? l.rows_many : KVX_ROWS_FEW,
                                                            (int64_t)it.q_len * l.group - it.row0);
-                    CHECK(joined[it.prow] == rows);
+                    CHECK(joined[it.prow + 16 * wave] == rows);
                 }
         CHECK(joined.size() == parts.size());
         std::set<std::pair<const int32_t *, int>> appended;

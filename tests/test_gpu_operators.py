@@ -215,6 +215,15 @@ def test_attention_split_over_the_keys(kind, held, dim):
         attend_case(c, [(1, 12001, 700), (30, 3000, 20)], 4, window=2000)
 
 
+@pytest.mark.parametrize("kind,held,dim", [("bf16", "bf16", 64), ("f16", "e4m3", 64), ("bf16", "bf16", 128),
+                                           ("f16", "f16", 80), ("bf16", "bf16", 256)])
+def test_attention_of_enough_work_for_a_head_a_wave(kind, held, dim):
+    """Token-major pages, heads a multiple of four, many or long sequences: cut and whole pieces."""
+    with Cache(heads=4, dim=dim, page=16, blocks=6200, kind=kind, cache=held) as c:
+        attend_case(c, [(1, 60000), (1, 23000), (3, 9000), (1, 130), (0, 5), (2, 1)], 8)
+        attend_case(c, [(1 + i % 3, 240 + i) for i in range(260)], 8, window=200 if dim == 64 else 0)
+
+
 @pytest.mark.parametrize("lens", [[(1, 700), (2, 300)], [(50, 400), (70, 100)]], ids=["few", "many"])
 @pytest.mark.parametrize("held", ["bf16", "e4m3"])
 @pytest.mark.parametrize("poison", [math.nan, math.inf])
