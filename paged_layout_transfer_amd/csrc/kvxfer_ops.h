@@ -18,7 +18,7 @@ namespace kvx {
 // ---- pages -------------------------------------------------------------------
 
 #define KVX_INLINE_COPIES 256  // records that ride in the kernel arguments (3 KiB)
-#define KVX_COPY_PART 8192     // bytes of a page one wave copies
+#define KVX_COPY_PART 4096     // bytes of a page one wave copies
 
 struct CopyLaunch {
     uint8_t *const *regions;     // of the first layer copied
