@@ -200,7 +200,7 @@ __device__ __forceinline__ Piece piece_of(const AttnLaunch &a, const AttnItem &i
 __device__ __forceinline__ RowMask row_mask(const AttnLaunch &a, const Piece &s, int32_t p)
 {
     RowMask m;
-    m.low = a.window > 0 ? p - a.window + 1 : 0;
+    m.low = a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
     m.high = a.full || p >= s.kv_len ? s.kv_len - 1 : p;
     m.prefix = s.prefix < s.kv_len ? s.prefix : s.kv_len;
     return m;
@@ -219,7 +219,7 @@ __device__ __forceinline__ bool all_see(const AttnLaunch &a, const Piece &s, int
 {
     if (j + n > s.kv_len) return false;
     if (a.full || j + n <= s.prefix) return true;
-    return j + n - 1 <= s.p0 && (a.window == 0 || j > s.p1 - a.window);
+    return j + n - 1 <= s.p0 && (a.window == 0 || s.p1 < a.window || j > s.p1 - a.window);
 }
 
 // The block that holds key j, and where key j's row (of the piece's head) starts in a region.  A

@@ -119,7 +119,7 @@ KVX_HD KeyWalk key_walk(int32_t kv_len, int32_t prefix, int32_t window, bool ful
     } else {
         w.prefix = prefix < kv_len ? prefix : kv_len;
         w.high = p1 + 1 < 0 ? 0 : p1 + 1;
-        w.low = window > 0 && p0 - window + 1 > 0 ? p0 - window + 1 : 0;
+        w.low = window > 0 && p0 >= window ? p0 - window + 1 : 0;
         if (w.low > w.high) w.low = w.high;
         if (w.prefix >= w.low) {  // one stretch
             if (w.prefix > w.high) w.high = w.prefix;

@@ -51,7 +51,7 @@ int main()
         d.head_dim = below(2) ? 64 : 256;
         a.num_q_heads = d.num_heads * (1 + (int32_t)below(9));
         const int mode = (int)below(4);
-        a.window = mode == 1 || mode == 3 ? 1 + (int32_t)below(300) : 0;
+        a.window = mode == 1 || mode == 3 ? (below(6) ? 1 + (int32_t)below(300) : INT32_MAX - (int32_t)below(3)) : 0;
         a.flags = mode == 2 ? KV_ATTN_FULL : 0;
         const int n = 1 + (int)below(6);
         std::vector<kv_seq> seqs;

@@ -171,7 +171,7 @@ def test_attention_pages_and_groups(page, heads, heads_q):
 
 
 VARIANTS = [
-    dict(window=1), dict(window=7), dict(window=64), dict(window=200), dict(full=True), dict(softcap=5.0),
+    dict(window=1), dict(window=2**31 - 1), dict(window=7), dict(window=64), dict(window=200), dict(full=True), dict(softcap=5.0),
     dict(slopes=True), dict(window=50, softcap=20.0, slopes=True), dict(full=True, slopes=True, softcap=3.0),
     dict(scale=0.0), dict(scale=-0.2), dict(scale=4.0),
 ]
