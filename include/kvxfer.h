@@ -473,49 +473,60 @@ KV_API int kv_remap_tables(kv_pool *pool, const kv_page_copy *moves, int32_t n, 
 
 /* ---- new tokens: append and attention -------------------------------------------- */
 
-/* A plan holds, on the device, one step's sequences, the split of their attention over the chip, and
- * the workspace of partial results; it is set once a step and used by every layer.  The
- * pool has num_kv 2, elem_bytes 1 for KV_TYPE_E4M3 and 2 else, head_dim <= KV_MAX_ATTN_DIM
- * (else KV_ERR_ARG), and head_dim * elem_bytes a multiple of 16 (KV_ERR_ALIGN).  create
- * allocates all device memory the plan will use, on the current device, which is then the
- * pool's; it must not be made while a stream captures (KV_ERR_HIP).  destroy waits for the device
- * to be idle first; NULL is accepted.  A plan is destroyed before its pool. */
+/* A plan holds, on the device, one step's sequences, the split of their attention over the
+ * chip, and the workspace of partial results (up to 200 MiB); it is set once a step and used
+ * by every layer.  The pool has num_kv 2, elem_bytes 1 for KV_TYPE_E4M3 and 2 else, head_dim <=
+ * KV_MAX_ATTN_DIM, and num_q_heads * max_tokens < 2^31 (else KV_ERR_ARG), and head_dim *
+ * elem_bytes a multiple of 16 (KV_ERR_ALIGN).  create allocates all device memory the plan
+ * will use, on the current device, which is then the pool's, and waits for the device; it must
+ * not be made while a stream captures (KV_ERR_HIP).  destroy waits for the device to be idle
+ * first; NULL is accepted.  A plan is destroyed before its pool, and graphs that hold its calls do not
+ * run again.  No passage for this section: the attention that reads the cache the pages move. */
 KV_API int kv_attn_plan_create(kv_pool *pool, const kv_attn_desc *desc, kv_attn_plan **out);
 KV_API int kv_attn_plan_destroy(kv_attn_plan *plan);
 
-/* Sets the plan to n (0 .. max_seqs) sequences: host work proportional to the
- * pieces of work, and one stream-ordered upload.  Errors: KV_ERR_ARG (negative lengths, null
- * table of a sequence with kv_len > 0, more sequences or rows than the plan holds), KV_ERR_RANGE (a table too
- * short or past its allocation, kv_len over its limit), KV_ERR_DUP (two sequences
- * own one row), KV_ERR_CAPTURE (the stream is capturing); the plan then stays as it was.
+/* Sets the plan to n (0 .. max_seqs) sequences: host work proportional to the pieces of work,
+ * and one stream-ordered upload.  Errors: KV_ERR_ARG (negative lengths, null table of a
+ * sequence with kv_len > 0, more sequences or new tokens than the plan holds, another device
+ * current), KV_ERR_ALIGN (a table not 4-byte aligned), KV_ERR_RANGE (a table too short or past
+ * its allocation, kv_len or a row over its limit), KV_ERR_DUP (two sequences own one row),
+ * KV_ERR_CAPTURE (the stream is capturing); the plan then stays as it was (after KV_ERR_HIP it has to
+ * be set again).  The tables stay the caller's and are read when append and attend run.
  * The calls that use one plan -- set, append, attend, replays of graphs they were captured
  * into -- share its memory: two that could overlap (different streams with no ordering
  * between them) must not be made. */
 KV_API int kv_attn_plan_set(kv_attn_plan *plan, const kv_seq *seqs, int32_t n, hipStream_t stream);
 
-/* Writes the new tokens' k and v rows into their pages of one layer: the token at position
- * p goes to slot p % block_size of block block_table[p / block_size].  An e4m3 pool gets x / scale, rounded to
- * nearest even and saturated at +-448; NaN stays NaN.  Rows of no sequence are not read.  KV_ERR_ARG when a
- * sequence has q_len > kv_len.  Two sequences must not write one pool token.  A block id out of
- * range is skipped and reported (kv_pool_get_error).
+/* Writes the new tokens' k and v rows into their pages of one layer: the token at position p
+ * goes to slot p % block_size of block block_table[p / block_size].  An e4m3 pool gets
+ * x / scale, rounded to nearest even and saturated at +-448; NaN stays NaN.  Nothing else is
+ * written, and rows of no sequence are not read.  Two sequences must not write one pool token.  A block id
+ * out of range is skipped and reported (kv_pool_get_error).  Errors: KV_ERR_ARG (layer, null or
+ * negative arguments, scales, a sequence with q_len > kv_len, another device current),
+ * KV_ERR_ALIGN, KV_ERR_RANGE (n_tokens below a row the plan names, an array past its allocation).
  * Append and attend make their launches and nothing else, so both can be captured into a
- * graph; a replay works on what the last kv_attn_plan_set on its stream set, within the arrays
- * the captured call named (rows past its n_tokens are neither read nor written). */
+ * graph; a replay works on what the last kv_attn_plan_set before it set, within the arrays
+ * the captured call named (rows past its n_tokens are neither read nor written; with a
+ * sequence of q_len > kv_len set, nothing is appended). */
 KV_API int kv_append_tokens(kv_attn_plan *plan, int32_t layer, const kv_append_args *args, hipStream_t stream);
 
 /* Attention of the new tokens over the cache of one layer.  With p = kv_len - q_len + i the
- * position of a query, it sees cached token j < kv_len where KV_ATTN_FULL is set, or j <
- * prefix_len, or j <= p and (window == 0 or j > p - window).  Scores are s = scale * k_scale *
- * <q, k_j>, then softcap * tanh(s / softcap) if softcap > 0, then s - slope * |p - j| if
- * slopes are given; out = v_scale * sum_j softmax(s)_j v_j, lse = log sum_j exp(s_j) (natural).
- * A query that sees nothing gets out = 0 and lse = -infinity.  Cached tokens that a query
- * does not see do not reach its result, whatever they hold (infinities and NaN too); pages
- * that no query sees are not read and their table entries may be anything.  Sums, maxima and
- * products are held in 32 bits; the weights are rounded to q_type for the second product.  Rows of no sequence are left as they
- * were.  The result does not depend on the run: no atomics take part.  The new tokens must
- * be in the cache already (kv_append_tokens on the same stream).  A block id out of range
- * is reported (kv_pool_get_error) and block 0 read in its place: the result of the queries that see it is
- * undefined.  Captured, a call holds the kernels for any sequences within the plan's limits. */
+ * position of a query, it sees cached token j < kv_len where KV_ATTN_FULL is set, or
+ * j < prefix_len, or j <= p and (window == 0 or j > p - window).  Scores are
+ * s = scale * k_scale * <q, k_j>, then softcap * tanh(s / softcap) if softcap > 0, then
+ * s - slope * |p - j| if slopes are given; out = v_scale * sum_j softmax(s)_j v_j,
+ * lse = log sum_j exp(s_j) (natural).  A query that sees nothing gets out = 0 and
+ * lse = -infinity.  Cached tokens that a query does not see do not reach its result, whatever
+ * they hold (infinities and NaN too); pages that no query sees are not read and their table entries
+ * may be anything.  Sums, maxima and both products' sums are held in 32 bits; the weights are rounded to
+ * q_type for the second product.  Rows of no sequence are left as they were.  The same call
+ * gives the same bits: no atomics take part, and split sums are joined in a fixed order.  The
+ * new tokens must be in the cache already (kv_append_tokens on the same stream).  out may be q
+ * itself, with its strides; it overlaps nothing else that the call reads.  A block id out of range is
+ * reported (kv_pool_get_error) and block 0 read in its place: the result of the queries that
+ * see it is undefined.  Errors: as kv_append_tokens; also KV_ERR_ARG for scale or softcap that are not
+ * finite, softcap < 0, scale / softcap over the 32-bit range, or rows of out that overlap.
+ * Captured, a call holds the kernels for any sequences within the plan's limits. */
 KV_API int kv_attend(kv_attn_plan *plan, int32_t layer, const kv_attend_args *args, hipStream_t stream);
 
 /* Synchronizes `stream`, then reads and clears the pool's sticky device error

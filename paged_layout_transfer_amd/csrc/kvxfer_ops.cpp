@@ -72,7 +72,7 @@ struct kv_attn_plan {
     kv_pool *pool = nullptr;
     kv_attn_desc desc{};
     kvx::PlanLimits lim{};
-    kvx::Plan plan;
+    kvx::Plan plan, next;  // the one set, and the one being made
     std::vector<std::pair<int64_t, int64_t>> rows;  // scratch: rows owned by the sequences
     kvx::ExtentCache extents;
     uint8_t *dev = nullptr, *host[2] = {nullptr, nullptr};
@@ -311,6 +311,7 @@ int kv_attn_plan_create(kv_pool *pool, const kv_attn_desc *desc, kv_attn_plan **
     p->lim = kvx::plan_limits(d, *desc);
     try {
         p->plan.reserve(p->lim);
+        p->next.reserve(p->lim);
         p->rows.reserve(desc->max_seqs);
     } catch (...) {
         delete p;
@@ -390,22 +391,28 @@ int kv_attn_plan_set(kv_attn_plan *p, const kv_seq *seqs, int32_t n, hipStream_t
             kvx::check_extent(p->extents, seqs[i].block_table, seqs[i].table_len * (int64_t)sizeof(int32_t)))
             return KV_ERR_RANGE;
     if (!HIP_OK(hipEventSynchronize(p->sent[p->turn]))) return KV_ERR_HIP;  // its last upload has left
-    kvx::build_plan(p->plan, p->lim, seqs, n);
+    kvx::Plan &plan = p->next;
+    try {
+        kvx::build_plan(plan, p->lim, seqs, n);  // within the vectors' capacities
+    } catch (...) {
+        return KV_ERR_OOM;
+    }
     uint8_t *h = p->host[p->turn];
     int64_t end = sizeof(kvx::PlanHead);
-    std::memcpy(h, &p->plan.head, sizeof(kvx::PlanHead));
+    std::memcpy(h, &plan.head, sizeof(kvx::PlanHead));
     auto put = [&](int64_t off, const auto &v) {
         if (v.empty()) return;
         std::memcpy(h + off, v.data(), v.size() * sizeof(v[0]));
         end = off + (int64_t)(v.size() * sizeof(v[0]));
     };
-    put(p->off_append, p->plan.append);
-    put(p->off_groups, p->plan.groups);
-    put(p->off_few, p->plan.few);
-    put(p->off_many, p->plan.many);
-    if (!HIP_OK(hipMemcpyAsync(p->dev, h, (size_t)end, hipMemcpyHostToDevice, stream)) ||
-        !HIP_OK(hipEventRecord(p->sent[p->turn], stream))) {
-        (void)hipStreamSynchronize(stream);
+    put(p->off_append, plan.append);
+    put(p->off_groups, plan.groups);
+    put(p->off_few, plan.few);
+    put(p->off_many, plan.many);
+    if (!HIP_OK(hipMemcpyAsync(p->dev, h, (size_t)end, hipMemcpyHostToDevice, stream))) return KV_ERR_HIP;
+    std::swap(p->plan, p->next);
+    if (!HIP_OK(hipEventRecord(p->sent[p->turn], stream))) {
+        (void)hipStreamSynchronize(stream);  // no fence: the image is free again once the stream has passed
         return KV_ERR_HIP;
     }
     p->turn ^= 1;
@@ -474,6 +481,7 @@ int kv_attend(kv_attn_plan *p, int32_t layer, const kv_attend_args *x, hipStream
     a.out_head = x->out_head_stride;
     a.scale_log2 = (float)((x->softcap > 0 ? 2 / (double)x->softcap : 1.0) * scale * log2e);
     a.cap_log2 = (float)(x->softcap * log2e);
+    if (!std::isfinite(a.scale_log2) || !std::isfinite(2 * a.cap_log2)) return KV_ERR_ARG;
     a.v_scale = e4m3 ? x->v_scale : 1.f;
     // a captured call holds every kernel that a plan within the limits may need
     for (int which = 0; which < 2; ++which) {

@@ -46,14 +46,15 @@ inline PlanLimits plan_limits(const kv_pool_desc &d, const kv_attn_desc &a)
     auto slices = [](int64_t n) { return (n + KVX_JOIN_ROWS - 1) / KVX_JOIN_ROWS; };
     const int64_t few = seqs * l.heads, cut_few = cut_parts(few, l.slots_few);
     l.cap_few = all_parts(few, l.slots_few);
-    l.cap_groups = cut_few / 2 * slices(std::min<int64_t>(rows, KVX_ROWS_FEW));
-    l.cap_prows = cut_few * KVX_ROWS_FEW * (l.heads % 4 == 0 ? 4 : 1);
-    l.cap_groups *= l.heads % 4 == 0 ? 4 : 1;
+    // a cut piece has two parts or more, and one record for KVX_JOIN_ROWS of its rows
+    const int64_t heads_cut = l.heads % 4 == 0 ? 4 : 1;  // of one piece (split_class: across)
+    l.cap_groups = std::min(cut_few / 2 * heads_cut, few) * slices(std::min<int64_t>(rows, KVX_ROWS_FEW));
+    l.cap_prows = cut_few * KVX_ROWS_FEW * heads_cut;
     l.cap_many = 0;
     if (rows > KVX_ROWS_FEW) {
         const int64_t many = (rows / l.rows_many + seqs) * l.heads, cut_many = cut_parts(many, kSlotsMany);
         l.cap_many = all_parts(many, kSlotsMany);
-        l.cap_groups += cut_many / 2 * slices(std::min<int64_t>(rows, l.rows_many));
+        l.cap_groups += std::min(cut_many / 2, many) * slices(std::min<int64_t>(rows, l.rows_many));
         l.cap_prows += cut_many * l.rows_many;
     }
     l.cap_append = a.max_tokens / KVX_APPEND_TOKENS + seqs;

@@ -356,6 +356,22 @@ def test_attention_is_the_same_from_run_to_run_and_on_another_stream():
                 assert torch.equal(words(lse[:rows]), words(first[1][:rows]))
 
 
+def test_the_result_may_take_the_queries_place():
+    with Cache(heads=2, dim=64, page=16, blocks=300, kind="bf16") as c:
+        lens = [(1, 700), (2, 3), (60, 900), (1, 3000)]
+        tables = [t.cuda() for t in deal(c, lens)]
+        seqs, rows = seqs_of(tables, lens)
+        plan = c.plan(8, len(lens), rows)
+        K.kv_attn_plan_set(plan, K.make_seqs(seqs))
+        q = torch.randn(rows, 8, 64, device="cuda").bfloat16()
+        out = torch.empty_like(q)
+        say("in place")
+        K.kv_attend(plan, 0, K.make_attend_args(q, out, n_tokens=rows, scale=0.125))
+        K.kv_attend(plan, 0, K.make_attend_args(q, q, n_tokens=rows, scale=0.125))
+        torch.cuda.synchronize()
+        assert torch.equal(words(q), words(out))
+
+
 def test_a_captured_step_works_on_the_plan_that_is_set_when_it_runs():
     """Append and attend of two layers captured once; each replay after another plan, with
     eager work in between, against the same calls made eagerly."""
@@ -524,6 +540,8 @@ def test_append_and_attend_refusals():
         attend(K.KV_ERR_ARG, n_tokens=-1)
         attend(K.KV_ERR_ARG, scale=math.nan)
         attend(K.KV_ERR_ARG, softcap=-1.0)
+        attend(K.KV_ERR_ARG, softcap=1e-42)                          # 2.9e41 times the dot product
+        attend(K.KV_ERR_ARG, softcap=3e38)
         attend(K.KV_ERR_ARG, k_scale=0.0)
         attend(K.KV_ERR_ARG, v_scale=math.inf)
         attend(K.KV_ERR_ARG, q=0)
