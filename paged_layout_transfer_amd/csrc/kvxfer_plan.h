@@ -93,13 +93,14 @@ inline int64_t parts_at(const std::vector<AttnItem> &whole, int64_t share, int32
 }
 
 // What splitting costs, in the time of one tile: a part's start and end, whole or cut, and the join.
-// Many rows: a cut part writes 128 KiB that the join reads, about three tiles each way at a
-// compute unit's share of HBM.  Few rows: a part's 8 KiB are nothing, but the join's launch takes 4 us,
-// ten tiles of a workgroup.
+// Many rows: a cut part writes up to 128 KiB that the join reads, a tile's time or two each way at a compute
+// unit's share of HBM (ragged 64-wide turns: 90 us at a cost of 2 or 4, 110 us at 6, where too
+// little is cut).  Few rows: a part's 8 KiB are nothing, but the join's launch takes 4 us, ten
+// tiles of a workgroup.
 struct SplitCost {
     int64_t whole, cut, join, min_tiles;
 };
-constexpr SplitCost kCostFew{2, 2, 10, 2}, kCostMany{1, 6, 2, 8};
+constexpr SplitCost kCostFew{2, 2, 10, 2}, kCostMany{1, 4, 2, 8};
 
 // When the last of `slots` workgroups ends, in tiles, if each takes the longest part left.
 // `ends` is scratch.
