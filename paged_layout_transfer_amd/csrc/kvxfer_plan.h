@@ -161,7 +161,8 @@ inline void split_class(Plan &p, std::vector<AttnItem> &out, const PlanLimits &l
         share = std::min(even, longest);
     } else {
         const int64_t lanes = std::max<int64_t>(1, slots / units);
-        int64_t best = span_at(p.whole, longest, lanes, cost, p.parts, p.ends);
+        const int64_t uncut = span_at(p.whole, longest, lanes, cost, p.parts, p.ends);
+        int64_t best = (uncut * 19 + 19) / 20;  // a cut for less than a twentieth is not worth its risk
         auto consider = [&](int64_t s) {
             if (s >= longest || parts_at(p.whole, s, units) > max_rounds(pieces, slots) * slots) return;
             const int64_t span = span_at(p.whole, s, lanes, cost, p.parts, p.ends);
