@@ -91,7 +91,7 @@ int launch_copy_pages(const CopyLaunch &a, hipStream_t stream)
 }
 
 // Table entries after moves: a binary search of each entry among the moves' sources, which sit
-// in shared memory when they fit.
+// in shared memory when they fit.  A million entries, 1024 moves: 10 us.
 template <bool LDS>
 __global__ __launch_bounds__(kThreads) void remap(const RemapLaunch a)
 {
@@ -141,8 +141,9 @@ __device__ __forceinline__ float e4m3_of(float x, float scale)
 }
 
 // One workgroup writes one item's tokens.  A thread owns eight values of a token's row (of its
-// keys, then its values) and goes over the tokens, four at a time: their block ids, then their rows,
-// then the stores.  Bound by the latency of that chain for a decode step's tokens, by HBM for a chunk's.
+// keys, then its values) and goes over the tokens, four at a time: their block ids and rows,
+// then the stores.  Bound by the latency of that chain: 3.5 us for 64 tokens of a decode step, 16 us
+// for 7874 tokens in chunks into an 8-bit pool (48 MB, 3 TB/s; one token at a time 22 us).
 template <class T, bool E4M3>
 __global__ __launch_bounds__(kThreads) void append_tokens(const AttnLaunch a)
 {
