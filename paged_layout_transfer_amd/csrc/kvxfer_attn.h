@@ -88,7 +88,7 @@ __device__ __forceinline__ typename Vec<T>::x4 from_e4m3(uint32_t w)
     return typename Vec<T>::x4{a[0], a[1], b[0], b[1]};
 }
 
-// The infinities and NaN among eight 16-bit values, one truth value each.
+// Whether a 16-bit value is an infinity or NaN.
 template <class T>
 __device__ __forceinline__ bool not_finite(uint16_t x)
 {
@@ -105,6 +105,7 @@ __device__ __forceinline__ bool any_not_finite(typename Vec<T>::x8 v)
     for (int i = 0; i < 4; ++i) bad |= ((w[i] & e) == e) | ((w[i] & (e << 16)) == (e << 16));
     return bad;
 }
+typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
 typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
 // The values with zeros for infinities and NaN.
 template <class T>
@@ -267,6 +268,10 @@ __device__ __forceinline__ void hide(X &x, const RowMask &mask, Key key)
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = mask.sees(key(i)) ? x[i] : -INFINITY;
 }
+
+// A factor for a row's sums, never zero: an infinity among them stays one however far the
+// maximum grows (zero times it would be NaN), and 2^-149 of anything else is nothing.
+__device__ __forceinline__ float keep(float by) { return fmaxf(by, 1.401298464e-45f); }
 
 // One query row's eight consecutive values, zero past the row's width.
 template <class T>
@@ -474,7 +479,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_few(const AttnL
             m = up;
             l *= by;
 #pragma unroll
-            for (int d = 0; d < DP / 16; ++d) o[d] *= by;
+            for (int d = 0; d < DP / 16; ++d) o[d] *= keep(by);
         }
         const float mm = m == -INFINITY ? 0.f : m * sc;
         T8 w;
@@ -536,7 +541,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_few(const AttnL
     }
     const float by = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mine - top);
 #pragma unroll
-    for (int d = 0; d < DP / 16; ++d) *(f32x4 *)((float *)tile + n * DP + d * 16 + 4 * g) = o[d] * by;
+    for (int d = 0; d < DP / 16; ++d) *(f32x4 *)((float *)tile + n * DP + d * 16 + 4 * g) = o[d] * keep(by);
     __syncthreads();
     const int at = across ? lane : (int)threadIdx.x, wide = across ? 4 : 16;  // threads of a row
     const int row = at / wide, w0 = across ? wave : 0, w1 = across ? wave + 1 : 4;
@@ -549,7 +554,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_few(const AttnL
     top = -INFINITY;
     for (int w = w0; w < w1; ++w) top = fmaxf(top, join_m[w][row]);
     for (int w = w0; w < w1; ++w)
-        if (join_m[w][row] != -INFINITY) sum += join_l[w][row] * __builtin_amdgcn_exp2f(join_m[w][row] - top);
+        sum += join_l[w][row] * (join_m[w][row] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(join_m[w][row] - top));
     for (int d = at % wide * 8; d < DP; d += wide * 8) {
         float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         for (int w = w0; w < w1; ++w)
@@ -741,7 +746,7 @@ __global__ __launch_bounds__(64 * many_waves<DP>(), DP == 64 ? 4 : DP == 128 ? 2
             m = up;
             l *= by;
 #pragma unroll
-            for (int d = 0; d < DP / 32; ++d) o[d] *= by;
+            for (int d = 0; d < DP / 32; ++d) o[d] *= keep(by);
         }
         const float mm = m == -INFINITY ? 0.f : m * sc;
         float sum[2] = {0.f, 0.f};
@@ -795,10 +800,11 @@ __global__ __launch_bounds__(64 * many_waves<DP>(), DP == 64 ? 4 : DP == 128 ? 2
 #pragma unroll
                     for (int b = 0; b < 4; ++b) {
                         const T4 v = *(const T4 *)(was + k * kV + 32 * d + 8 * b + 4 * g);
+                        // the whole vector: a bit cast of one element reads element 0
+                        const u16x4 bits = __builtin_bit_cast(u16x4, v);
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            o[d][4 * b + e] +=
-                                seen && not_finite<T>(__builtin_bit_cast(uint16_t, v[e])) ? (float)v[e] : 0.f;
+                            o[d][4 * b + e] += seen && not_finite<T>(bits[e]) ? (float)v[e] : 0.f;
                     }
             }
         }
@@ -897,13 +903,16 @@ __global__ __launch_bounds__(256) void join(const AttnLaunch a)
         const float pm = a.part_ml[2 * at], pl = a.part_ml[2 * at + 1];
         const f32x4 x = *(const f32x4 *)(a.part_o + at * DP + d), y = *(const f32x4 *)(a.part_o + at * DP + d + 4);
         const float up = fmaxf(m, pm);
-        // a part that saw nothing holds zeros and no maximum
+        // a part that saw nothing holds zeros and no maximum (or NaN, from a score that is none)
         const float was = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - up);
         const float by = pm == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(pm - up);
         m = up;
         l = l * was + pl * by;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = v[i] * was + x[i] * by, v[4 + i] = v[4 + i] * was + y[i] * by;
+        for (int i = 0; i < 4; ++i) {
+            v[i] = v[i] * keep(was) + x[i] * keep(by);
+            v[4 + i] = v[4 + i] * keep(was) + y[i] * keep(by);
+        }
     }
     if (kLanes > 1) {
         if (d == 0) share_m[k0][row] = m, share_l[k0][row] = l;
@@ -922,7 +931,7 @@ __global__ __launch_bounds__(256) void join(const AttnLaunch a)
             const float by = share_m[k][row] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(share_m[k][row] - m);
             l += share_l[k][row] * by;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += share_v[k][row][d + i] * by;
+            for (int i = 0; i < 8; ++i) v[i] += share_v[k][row][d + i] * keep(by);
         }
     }
     if (!live) return;

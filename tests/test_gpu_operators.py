@@ -143,6 +143,7 @@ def attend_case(cache, lens, heads_q, *, window=0, full=False, softcap=0.0, slop
         assert not bad.any(), "out: %d of %d off, worst %g of %g allowed" % (
             bad.sum(), bad.numel(), (g - want).abs()[fin].max(), tol[fin][(g - want).abs()[fin].argmax()])
         some = torch.isfinite(z)
+        assert torch.equal(torch.isnan(gz), torch.isnan(z))
         assert torch.equal(gz[~some & ~torch.isnan(z)], z[~some & ~torch.isnan(z)])
         assert ((gz - z).abs()[some] <= tol_z[some]).all(), "lse: worst %g" % (gz - z).abs()[some].max()
     return plan, args, out, lse, (tables_d, q_d, sl_d)      # what the plan and the arguments point at
@@ -246,6 +247,35 @@ def test_what_a_query_does_not_see_does_not_reach_it(lens, held, poison):
             bits[:, ~keep] = torch.tensor([poison]).to(view.dtype).view(bits.dtype)
             c.upload()
             attend_case(c, lens, 4, window=window, label="poison %s" % poison)
+
+
+@pytest.mark.parametrize("lens", [[(1, 20), (3, 300)], [(50, 60), (70, 400)]], ids=["few", "many"])
+@pytest.mark.parametrize("window", [0, 40])
+def test_infinite_and_nan_values_reach_the_queries_that_see_them(lens, window):
+    """Values (not keys) of single cached tokens: the first one, one in the middle and the
+    newest, an infinity of either sign, both in one column, NaN."""
+    with Cache(heads=2, dim=64, page=16, blocks=60, kind="bf16") as c:
+        for t, (q, n) in zip(deal(c, lens), lens):
+            at = lambda j: c.host[1][int(t[j // 16]), j % 16]       # noqa: E731
+            at(0)[0, 3] = math.inf
+            at(n // 2)[0, 5] = -math.inf
+            at(n - 1)[1, 7] = math.nan
+            at(n - 1)[0, 9] = math.inf
+            at(n - 2)[0, 9] = -math.inf
+            at(n - 2)[1, 11] = math.inf
+        c.upload()
+        attend_case(c, lens, 4, window=window, label="infinite values")
+
+
+def test_a_nan_key_reaches_the_queries_that_see_it():
+    """Alone in its stretch of keys, so that the wave or part that meets it has no other score."""
+    for lens in ([(1, 257), (1, 1), (2, 1500)], [(70, 1025)]):
+        with Cache(heads=2, dim=64, page=16, blocks=150, kind="bf16") as c:
+            for t, (q, n) in zip(deal(c, lens), lens):
+                c.host[0][int(t[(n - 1) // 16]), (n - 1) % 16, 1] = math.nan
+            c.upload()
+            attend_case(c, lens, 4, window=1 if len(lens) > 1 else 0, label="NaN key")
+            attend_case(c, lens, 4, label="NaN key")
 
 
 def test_tables_of_unseen_pages_may_hold_anything():
