@@ -594,7 +594,7 @@ constexpr int many_lds() { return KVX_TILE_KEYS * (2 * (key_row<DP>() + value_ro
 // i + 4 are fetched by another.  One barrier a tile.
 // Bound by the matrix pipe and the vector pipe together (one exponential and four other
 // operations for each score): of the cycles a compute unit is busy the matrix pipe works 46 %, the
-// vector pipe a third, and the two of one SIMD overlap only in part (56 vector operations beside 8
+// vector pipe 42 %, and the two of one SIMD overlap only in part (56 vector operations beside 8
 // products take 375 cycles, alone 156 and 292).  Eight waves share a tile so that shared memory is read
 // for 256 rows at a time, with no bank conflict; two workgroups of four waves took 15 % longer,
 // and half of the waves half a tile behind the others gained nothing.  Measured, bf16, 32 query heads on 8 of
