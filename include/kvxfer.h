@@ -300,7 +300,8 @@ KV_API int kv_pool_create(const kv_pool_desc *desc, kv_pool **out);
 
 /* Frees the handle and its device state, after waiting for the transfers it
  * queued that are still in flight (their fence events; other device work is not
- * waited for, nor are replays of calls captured into graphs: those must have finished,
+ * waited for, unless the pool has copied pages or rewritten tables: then the device is idle
+ * first; nor are replays of calls captured into graphs: those must have finished,
  * and such graphs must not run again).  The caller's regions are untouched.  NULL is
  * accepted.
  * No passage: library infrastructure (the handle's lifetime). */

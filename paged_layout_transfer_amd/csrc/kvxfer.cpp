@@ -381,9 +381,18 @@ using kvx::device_setup;
 
 void device_teardown(kv_pool *p)
 {
-    // Every launch that reads the pool's device state (region table, error word,
-    // span records) is fenced by its arena event, so waiting for the calls still in
-    // flight is enough; other work on the device is left alone.
+    // Every transfer's launch that reads the pool's device state (region table, error
+    // word, span records) is fenced by its arena event, so waiting for the calls still in
+    // flight is enough and other work on the device is left alone, unless the pool has
+    // made calls with no event.
+    if (p->unfenced) {
+        int dev = -1;
+        const bool other = hipGetDevice(&dev) == hipSuccess && dev != p->device;
+        if (other) (void)hipSetDevice(p->device);
+        (void)hipDeviceSynchronize();
+        if (other) (void)hipSetDevice(dev);
+        (void)hipGetLastError();
+    }
     if (p->device >= 0)
         for (int k = 0; k < p->arena.count; ++k)
             (void)hipEventSynchronize(p->fl_ev[(p->arena.first + k) % kInflight]);

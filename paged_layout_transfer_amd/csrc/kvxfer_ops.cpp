@@ -33,8 +33,9 @@ int capturing(hipStream_t stream, bool *out)
     return KV_OK;
 }
 
-// Launches with the call's records: in the kernel arguments (n <= KVX_INLINE_COPIES) or through
-// the pool's arena, whose stretch also fences the call for kv_pool_destroy.
+// Launches with the call's records: in the kernel arguments (n <= KVX_INLINE_COPIES), with no event
+// behind them, which would cost 3 us of a call's 10 (kv_pool_destroy waits for the device instead);
+// or through the pool's arena, whose stretch also fences the call.
 template <class Rec, class Args, class Launch>
 int launch_with_records(kv_pool *p, const Rec *recs, int32_t n, Args &a, const Rec *Args::*dev, hipStream_t stream,
                         Launch launch)
@@ -45,18 +46,19 @@ int launch_with_records(kv_pool *p, const Rec *recs, int32_t n, Args &a, const R
     if (int rc = kvx::check_regions(p)) return rc;
     if (int rc = kvx::device_setup(p)) return rc;
     a.*dev = nullptr;
-    if (n <= KVX_INLINE_COPIES) std::memcpy(a.inl, recs, (size_t)n * sizeof(Rec));
-    if (cap) return kvx::hip_ok((hipError_t)launch(), "hipLaunchKernel") ? KV_OK : KV_ERR_HIP;
+    if (n <= KVX_INLINE_COPIES) {
+        std::memcpy(a.inl, recs, (size_t)n * sizeof(Rec));
+        p->unfenced |= !cap;
+        return kvx::hip_ok((hipError_t)launch(), "hipLaunchKernel") ? KV_OK : KV_ERR_HIP;
+    }
     const int64_t bytes = ((int64_t)n * (int64_t)sizeof(Rec) + 255) & ~255LL;
     int64_t off = 0;
     if (int rc = kvx::arena_take(p, bytes, &off)) return rc;
-    if (n > KVX_INLINE_COPIES) {
-        std::memcpy(p->h_arena + off, recs, (size_t)n * sizeof(Rec));
-        if (!HIP_OK(hipMemcpyAsync(p->d_arena + off, p->h_arena + off, (size_t)n * sizeof(Rec), hipMemcpyHostToDevice,
-                                   stream)))
-            return KV_ERR_HIP;
-        a.*dev = reinterpret_cast<const Rec *>(p->d_arena + off);
-    }
+    std::memcpy(p->h_arena + off, recs, (size_t)n * sizeof(Rec));
+    if (!HIP_OK(hipMemcpyAsync(p->d_arena + off, p->h_arena + off, (size_t)n * sizeof(Rec), hipMemcpyHostToDevice,
+                               stream)))
+        return KV_ERR_HIP;
+    a.*dev = reinterpret_cast<const Rec *>(p->d_arena + off);
     if (!kvx::hip_ok((hipError_t)launch(), "hipLaunchKernel")) {
         (void)hipStreamSynchronize(stream);  // the copy may be in flight: its stretch is free again
         return KV_ERR_HIP;

@@ -47,6 +47,7 @@ struct kv_pool {
     uint8_t *h_arena = nullptr;
     kvx::ArenaRing<kvx::kInflight> arena;
     hipEvent_t fl_ev[kvx::kInflight] = {};  // one per arena slot
+    bool unfenced = false;  // calls were made with no event behind them: destroy waits for the device
     // staging-memory kind of the last staging base seen
     kvx::StagingKind staging_kind;
     // the declared extents of the regions, staging bases and block tables against

@@ -742,3 +742,23 @@ def test_a_request_forks_grows_is_compacted_and_answers_the_same(kind, held):
         out = step(again.cuda(), [(tables[n], 8, 102, n, 1) for n in range(3)])
         assert torch.equal(words(out), words(plain))
         assert K.kv_pool_get_error(c.handle, stream) == 0
+
+
+def test_a_pool_destroyed_behind_its_page_copies():
+    """Copies and rewritten tables have no event of their own: destroy waits for the device."""
+    region = torch.arange(64 * 4096, dtype=torch.int32, device="cuda").view(64, 4096)    # 16 KiB pages
+    want, table = region.clone(), torch.arange(64, dtype=torch.int32, device="cuda")
+    side, big = torch.cuda.Stream(), torch.ones(1 << 26, device="cuda")
+    pool = K.kv_pool_create(K.make_pool_desc(1, 1, 8, 128, 1, 16, 64, 16384, [region]))
+    torch.cuda.synchronize()
+    copies = K.make_page_copies([(i, 32 + i, 16) for i in range(8)])
+    say("copies behind other work, then destroy")
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            big.mul_(1.0)
+        K.kv_copy_pages(pool, copies, 0, 1, side)
+        K.kv_remap_tables(pool, copies, table, table, 64, side)
+    K.kv_pool_destroy(pool)
+    assert side.query()
+    want[32:40] = want[:8]
+    assert torch.equal(region, want) and table[:8].tolist() == list(range(32, 40)) and table[8:].tolist() == list(range(8, 64))
