@@ -175,7 +175,6 @@ struct Piece {
     KeyWalk walk;
 };
 
-template <int ROWS>
 __device__ __forceinline__ Piece piece_of(const AttnLaunch &a, const AttnItem &it)
 {
     Piece s;
@@ -190,7 +189,7 @@ __device__ __forceinline__ Piece piece_of(const AttnLaunch &a, const AttnItem &i
     s.tile1 = it.tile1;
     s.prow = it.prow;
     s.rows = s.q_len * a.group - s.row0;
-    if (s.rows > ROWS) s.rows = ROWS;
+    if (s.rows > it.rows) s.rows = it.rows;
     s.first = s.kv_len - s.q_len;
     s.p0 = s.first + (int32_t)div_by(s.row0, a.group_magic, a.group_shift);
     s.p1 = s.first + (int32_t)div_by(s.row0 + s.rows - 1, a.group_magic, a.group_shift);
@@ -342,7 +341,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_few(const AttnL
     const int32_t n_few = plan_record(a.head).n_few;
     asm volatile("" : : "s"(it.kv_len), "s"(n_few));  // both on their way before either is waited for
     if ((int32_t)blockIdx.x >= n_few) return;
-    Piece s = piece_of<16>(a, it);
+    Piece s = piece_of(a, it);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const bool across = it.across != 0;
     if (across) {
@@ -619,7 +618,7 @@ __global__ __launch_bounds__(64 * many_waves<DP>(), DP == 64 ? 4 : DP == 128 ? 2
 
     const AttnItem it = plan_record(a.items + blockIdx.x);
     if ((int32_t)blockIdx.x >= plan_record(a.head).n_many) return;
-    const Piece s = piece_of<32 * kWaves>(a, it);
+    const Piece s = piece_of(a, it);
     const int32_t n_tiles = s.tile1 - s.tile0;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int n = lane & 31, g = lane >> 5;

@@ -65,8 +65,10 @@ int launch_remap(const RemapLaunch &a, hipStream_t stream);
 // Rows of a piece of the many-rows kernel: 32 to a wave; at the widest heads a wave's
 // registers leave room for four waves only.
 KVX_HD int32_t rows_many(int dim) { return dim > 128 ? 128 : 256; }
+// With fewer rows, every second wave only helps loading (chosen by build_plan).
+#define KVX_ROWS_HALF 128
 
-// One workgroup's piece of attention: rows [row0, row0 + rows of the kernel) of one
+// One workgroup's piece of attention: rows [row0, row0 + rows) of one
 // sequence and cache head, over key tiles [tile0, tile1) of the tiles any of its rows sees.
 // Row r is query token r / G with head `head` * G + r % G, G query heads to a cache head.
 struct AttnItem {
@@ -74,7 +76,8 @@ struct AttnItem {
     int32_t kv_len, q_begin, q_len, prefix;
     int32_t head, row0, tile0, tile1;
     int32_t prow;    // first row in the workspace of partial results, or -1: the result is whole
-    int32_t across;  // few rows: the four waves take the cache heads head .. head + 3 instead of
+    int16_t rows;    // rows of the piece, unless the sequence's end first
+    int16_t across;  // few rows: the four waves take the cache heads head .. head + 3 instead of
                      // every fourth step of one head; wave w's partial rows lie 16 w behind prow
 };
 static_assert(sizeof(AttnItem) == 48, "");

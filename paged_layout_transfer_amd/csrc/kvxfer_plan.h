@@ -22,8 +22,8 @@ struct PlanLimits {
 };
 
 // Capacities that hold any plan of max_seqs sequences and max_tokens new tokens.  Of a class
-// with at most `pieces` pieces, split_class cuts at most cut_parts() parts, and makes at most all_parts()
-// parts in all.
+// with at most `pieces` pieces, at most cut_parts() parts are cut, and at most all_parts()
+// made in all.
 inline int64_t max_rounds(int64_t pieces, int64_t slots) { return pieces <= slots ? 2 : 4; }
 inline int64_t cut_parts(int64_t pieces, int64_t slots) { return max_rounds(pieces, slots) * slots; }
 inline int64_t all_parts(int64_t pieces, int64_t slots)
@@ -47,7 +47,7 @@ inline PlanLimits plan_limits(const kv_pool_desc &d, const kv_attn_desc &a)
     const int64_t few = seqs * l.heads, cut_few = cut_parts(few, l.slots_few);
     l.cap_few = all_parts(few, l.slots_few);
     // a cut piece has two parts or more, and one record for KVX_JOIN_ROWS of its rows
-    const int64_t heads_cut = l.heads % 4 == 0 ? 4 : 1;  // of one piece (split_class: across)
+    const int64_t heads_cut = l.heads % 4 == 0 ? 4 : 1;  // of one piece (Split::across)
     l.cap_groups = std::min(cut_few / 2 * heads_cut, few) * slices(std::min<int64_t>(rows, KVX_ROWS_FEW));
     l.cap_prows = cut_few * KVX_ROWS_FEW * heads_cut;
     l.cap_many = 0;
@@ -95,12 +95,16 @@ inline int64_t parts_at(const std::vector<AttnItem> &whole, int64_t share, int32
 // What splitting costs, in the time of one tile: a part's start and end, whole or cut, and the join.
 // Many rows: a cut part writes up to 128 KiB that the join reads, a tile's time or two each way at a compute
 // unit's share of HBM (ragged 64-wide turns: 90 us at a cost of 2 or 4, 110 us at 6, where too
-// little is cut).  Few rows: a part's 8 KiB are nothing, but the join's launch takes 4 us, ten
+// little is cut); the join's launch two to four (with 2 prompts of 1024 and 1536 tokens were cut,
+// 38.7 and 50 us, and now are not).  Few rows: a part's 8 KiB are nothing, but the join's 4 us are ten
 // tiles of a workgroup.
 struct SplitCost {
     int64_t whole, cut, join, min_tiles;
 };
-constexpr SplitCost kCostFew{2, 2, 10, 2}, kCostMany{1, 4, 2, 8};
+constexpr SplitCost kCostFew{2, 2, 10, 2}, kCostMany{1, 4, 4, 8}, kCostHalf{1, 4, 5, 8};
+// A tile with half of the waves at work takes 72 hundredths of the time of one with all (1.5 and
+// 2.1 us, 128-wide heads; 512 new tokens on 16 K cached, cut to one round either way: 217 and 155 us).
+constexpr int64_t kHalfTile = 72;
 
 // When the last of `slots` workgroups ends, in tiles, if each takes the longest part left.
 // `ends` is scratch.
@@ -131,11 +135,16 @@ inline int64_t span_at(const std::vector<AttnItem> &whole, int64_t share, int64_
 //    share tiles gives at most t / share + 1 < 2 t / share parts, and the sum of t / share is at
 //    most slots.
 //  * Fewer: no cut, the smallest share whose parts fill one, two, ... rounds, or the longest piece
-//    cut in two, three or four and the others where they are longer, whichever ends first.  One round suits equal pieces; more even out unequal ones (32 sequences of 1 K to
-//    64 K tokens: one round 353 us, two 335 us, four 333 us; one sequence of 32 K: 34, 38, 49 us).
+//    cut in two, three or four and the others where they are longer, whichever ends first.  One
+//    round suits equal pieces; more even out unequal ones (32 sequences of 1 K to 64 K tokens: one
+//    round 353 us, two 335 us, four 333 us; one sequence of 32 K: 34, 38, 49 us).
 // Without the costs of a cut, a prompt of 2048 tokens was cut into parts of 11 tiles and took 68 us.
-inline void split_class(Plan &p, std::vector<AttnItem> &out, const PlanLimits &l, int32_t rows_of_piece,
-                        int64_t slots, const SplitCost &cost, bool few, int64_t *prow)
+struct Split {
+    int64_t share, span;  // tiles of a part at most; when the last workgroup ends, in tiles (0: not asked)
+    int32_t across;       // cache heads of a workgroup
+};
+inline Split choose_split(Plan &p, const PlanLimits &l, int64_t slots, const SplitCost &cost, bool few,
+                          int64_t parts_max = INT64_MAX)
 {
     int64_t total = 0, longest = 1;
     for (const AttnItem &it : p.whole)
@@ -147,6 +156,7 @@ inline void split_class(Plan &p, std::vector<AttnItem> &out, const PlanLimits &l
     total /= across;
     const int64_t even = std::max(cost.min_tiles, (total + slots - 1) / slots);
     const int64_t pieces = (int64_t)p.whole.size() * units;
+    parts_max = std::min(parts_max, cut_parts(pieces, slots));
     auto fitting = [&](int64_t parts) {
         int64_t lo = std::min(cost.min_tiles, longest), hi = longest;
         while (lo < hi) {
@@ -156,22 +166,32 @@ inline void split_class(Plan &p, std::vector<AttnItem> &out, const PlanLimits &l
         }
         return lo;
     };
-    int64_t share = longest;
+    Split out{longest, 0, across};
     if (pieces >= 4 * slots) {
-        share = std::min(even, longest);
+        out.share = std::min(even, longest);
     } else {
         const int64_t lanes = std::max<int64_t>(1, slots / units);
         const int64_t uncut = span_at(p.whole, longest, lanes, cost, p.parts, p.ends);
+        out.span = uncut;
         int64_t best = (uncut * 19 + 19) / 20;  // a cut for less than a twentieth is not worth its risk
         auto consider = [&](int64_t s) {
-            if (s >= longest || parts_at(p.whole, s, units) > max_rounds(pieces, slots) * slots) return;
+            if (s >= longest || parts_at(p.whole, s, units) > parts_max) return;
             const int64_t span = span_at(p.whole, s, lanes, cost, p.parts, p.ends);
-            if (span < best) best = span, share = s;
+            if (span < best) out.span = best = span, out.share = s;
         };
-        for (int64_t rounds = 1; rounds <= max_rounds(pieces, slots); ++rounds)
+        for (int64_t rounds = 1; rounds * slots <= parts_max; ++rounds)
             if (pieces <= rounds * slots) consider(fitting(rounds * slots));
         for (int64_t cuts = 2; cuts <= 4; ++cuts) consider(std::max(cost.min_tiles, (longest + cuts - 1) / cuts));
     }
+    return out;
+}
+
+// The parts of the pieces in `whole`, longest first, and the records that join them.
+inline void cut(Plan &p, std::vector<AttnItem> &out, const PlanLimits &l, int32_t rows_of_piece, const Split &split,
+                int64_t *prow)
+{
+    const int64_t share = split.share;
+    const int32_t across = split.across, units = l.heads / across;
     for (const AttnItem &it : p.whole) {
         const int64_t n = (it.tile1 + share - 1) / share;
         const int32_t rows = (int32_t)std::min<int64_t>(rows_of_piece, (int64_t)it.q_len * l.group - it.row0);
@@ -205,6 +225,37 @@ inline void split_class(Plan &p, std::vector<AttnItem> &out, const PlanLimits &l
     });
 }
 
+// The pieces of the few rows' or the many rows' sequences into `whole`, `step` rows each; the largest's rows.
+inline int32_t pieces_of(Plan &p, const PlanLimits &l, const kv_seq *seqs, int32_t n, bool few, int32_t step)
+{
+    int32_t most = 0;
+    p.whole.clear();
+    for (int32_t i = 0; i < n; ++i) {
+        const kv_seq &s = seqs[i];
+        const int64_t rows = (int64_t)s.q_len * l.group;
+        if (rows == 0 || (rows <= KVX_ROWS_FEW) != few) continue;
+        most = std::max(most, (int32_t)std::min<int64_t>(rows, step));
+        for (int64_t r = 0; r < rows; r += step) {
+            const int32_t t0 = (int32_t)(r / l.group);
+            const int32_t t1 = (int32_t)((std::min(rows, r + step) - 1) / l.group);
+            const int32_t first = (int32_t)(s.kv_len - s.q_len);
+            const KeyWalk w = key_walk((int32_t)s.kv_len, s.prefix_len, l.window, l.full, first + t0, first + t1);
+            AttnItem it{};
+            it.table = s.block_table;
+            it.kv_len = (int32_t)s.kv_len;
+            it.q_begin = (int32_t)s.q_begin;
+            it.q_len = s.q_len;
+            it.prefix = s.prefix_len;
+            it.row0 = (int32_t)r;
+            it.tile1 = w.n_tiles;
+            it.prow = -1;
+            it.rows = (int16_t)step;
+            p.whole.push_back(it);
+        }
+    }
+    return most;
+}
+
 // The plan of checked sequences.
 inline void build_plan(Plan &p, const PlanLimits &l, const kv_seq *seqs, int32_t n)
 {
@@ -215,33 +266,24 @@ inline void build_plan(Plan &p, const PlanLimits &l, const kv_seq *seqs, int32_t
     p.tokens_end = 0;
     p.appendable = true;
     int64_t prow = 0;
-    for (int cls = 0; cls < 2; ++cls) {
-        const bool few = cls == 0;
-        const int32_t step = few ? KVX_ROWS_FEW : l.rows_many;
-        p.whole.clear();
-        for (int32_t i = 0; i < n; ++i) {
-            const kv_seq &s = seqs[i];
-            const int64_t rows = (int64_t)s.q_len * l.group;
-            if (rows == 0 || (rows <= KVX_ROWS_FEW) != few) continue;
-            for (int64_t r = 0; r < rows; r += step) {
-                const int32_t t0 = (int32_t)(r / l.group);
-                const int32_t t1 = (int32_t)((std::min(rows, r + step) - 1) / l.group);
-                const int32_t first = (int32_t)(s.kv_len - s.q_len);
-                const KeyWalk w =
-                    key_walk((int32_t)s.kv_len, s.prefix_len, l.window, l.full, first + t0, first + t1);
-                AttnItem it{};
-                it.table = s.block_table;
-                it.kv_len = (int32_t)s.kv_len;
-                it.q_begin = (int32_t)s.q_begin;
-                it.q_len = s.q_len;
-                it.prefix = s.prefix_len;
-                it.row0 = (int32_t)r;
-                it.tile1 = w.n_tiles;
-                it.prow = -1;
-                p.whole.push_back(it);
+    if (pieces_of(p, l, seqs, n, true, KVX_ROWS_FEW) > 0)
+        cut(p, p.few, l, KVX_ROWS_FEW, choose_split(p, l, l.slots_few, kCostFew, true), &prow);
+    int32_t step = l.rows_many;
+    if (const int32_t rows = pieces_of(p, l, seqs, n, false, step)) {
+        Split split = choose_split(p, l, kSlotsMany, kCostMany, false);
+        // Half the rows in twice as many pieces, at most two to a workgroup that runs at once, for steps
+        // that do not fill the chip otherwise.  128-wide heads, 32 on 8: a prompt of 256 tokens 17.4 -> 13.8
+        // us, of 1024 38.6 -> 31.7, of 2048 67.7 -> 65.3; 1024 new on 5000 through a window of 1000 43 -> 36;
+        // worst seen, six ragged sequences of 40 to 1500 new tokens, 52 -> 56.
+        if (rows > KVX_ROWS_HALF && split.span) {
+            pieces_of(p, l, seqs, n, false, KVX_ROWS_HALF);
+            if ((int64_t)p.whole.size() * l.heads <= 2 * kSlotsMany) {
+                const Split half = choose_split(p, l, kSlotsMany, kCostHalf, false, 2 * kSlotsMany);
+                if (half.span * kHalfTile < split.span * 100) split = half, step = KVX_ROWS_HALF;
             }
+            if (step != KVX_ROWS_HALF) pieces_of(p, l, seqs, n, false, step);
         }
-        split_class(p, few ? p.few : p.many, l, step, few ? l.slots_few : kSlotsMany, few ? kCostFew : kCostMany, few, &prow);
+        cut(p, p.many, l, step, split, &prow);
     }
     for (int32_t i = 0; i < n; ++i) {
         const kv_seq &s = seqs[i];

@@ -85,7 +85,8 @@ int main()
                 CHECK(!whole.across || !cls);
                 it.head += wave;
                 if (it.prow >= 0) it.prow += 16 * wave;
-                const int step = cls ? l.rows_many : KVX_ROWS_FEW;
+                const int step = it.rows;
+                CHECK(step == (cls ? l.rows_many : KVX_ROWS_FEW) || (cls && step == KVX_ROWS_HALF));
                 CHECK(it.head >= 0 && it.head < d.num_heads && it.row0 % step == 0);
                 const int64_t rows = std::min<int64_t>(step, (int64_t)it.q_len * l.group - it.row0);
                 CHECK(rows > 0);
@@ -131,7 +132,7 @@ int main()
         for (int cls = 0; cls < 2; ++cls)
             for (const AttnItem &it : cls ? p.many : p.few)
                 for (int wave = 0; it.prow >= 0 && wave < (it.across ? 4 : 1); ++wave) {
-                    const int64_t rows = std::min<int64_t>(cls ? l.rows_many : KVX_ROWS_FEW,
+                    const int64_t rows = std::min<int64_t>(it.rows,
                                                            (int64_t)it.q_len * l.group - it.row0);
                     CHECK(joined[it.prow + 16 * wave] == rows);
                 }
@@ -153,6 +154,48 @@ int main()
         }
         CHECK(appended.size() == (p.appendable ? news : 0));
     }
+    // counts alone, of larger steps: half pieces and whole ones, cut and uncut
+    int halves = 0, wholes = 0, cuts = 0;
+    for (int round = 0; round < 1500; ++round) {
+        kv_pool_desc d{};
+        d.num_heads = 1 + (int32_t)below(8);
+        d.page_layout = KV_PAGE_TOKEN_MAJOR;
+        d.block_size = 16;
+        kv_attn_desc a{};
+        d.head_dim = below(4) ? 128 : 256;
+        a.num_q_heads = d.num_heads * (1 + (int32_t)below(8));
+        a.window = below(4) ? 0 : 1 + (int32_t)below(5000);
+        std::vector<kv_seq> seqs;
+        int64_t at = 0;
+        const int n = 1 + (int)below(below(2) ? 3 : 40);
+        for (int i = 0; i < n; ++i) {
+            kv_seq s{};
+            s.block_table = (const int32_t *)(uintptr_t)4096;
+            s.q_len = (int32_t)(below(3) ? 1 + below(1 << below(13)) : 1);
+            s.kv_len = s.q_len + (below(2) ? below(1 << below(18)) : 0);
+            s.q_begin = at;
+            at += s.q_len;
+            seqs.push_back(s);
+        }
+        a.max_seqs = n;
+        a.max_tokens = at;
+        const PlanLimits l = plan_limits(d, a);
+        Plan p;
+        build_plan(p, l, seqs.data(), n);
+        CHECK((int64_t)p.few.size() <= l.cap_few && (int64_t)p.many.size() <= l.cap_many);
+        CHECK((int64_t)p.groups.size() <= l.cap_groups && (int64_t)p.append.size() <= l.cap_append);
+        int64_t rows = 0, want = 0;
+        for (int cls = 0; cls < 2; ++cls)
+            for (const AttnItem &it : cls ? p.many : p.few) {
+                const int64_t r = std::min<int64_t>(it.rows, (int64_t)it.q_len * l.group - it.row0);
+                if (it.prow >= 0) CHECK(it.prow + (int64_t)it.rows * (it.across ? 4 : 1) <= l.cap_prows);
+                if (it.tile0 == 0) rows += r * (it.across ? 4 : 1);
+                if (cls) halves += it.rows < l.rows_many, wholes += it.rows == l.rows_many, cuts += it.prow >= 0;
+            }
+        for (const kv_seq &s : seqs) want += (int64_t)s.q_len * l.group * d.num_heads;
+        CHECK(rows == want);
+    }
+    CHECK(halves > 1000 && wholes > 1000 && cuts > 1000);
     std::printf("ok\n");
     return 0;
 }

@@ -267,6 +267,17 @@ def test_infinite_and_nan_values_reach_the_queries_that_see_them(lens, window):
         attend_case(c, lens, 4, window=window, label="infinite values")
 
 
+@pytest.mark.parametrize("n", [6, 34], ids=["half_pieces", "whole_pieces"])
+@pytest.mark.parametrize("dim,kind,cache", [(64, "f16", "f16"), (128, "bf16", "e4m3")])
+def test_pieces_of_128_and_256_rows(n, dim, kind, cache):
+    """A step that does not fill the chip is planned in pieces of half the rows."""
+    lens = [(66 + i % 3, 66 + 7 * i) for i in range(1, n)] + [(66, 66)]
+    with Cache(heads=8, dim=dim, page=16, blocks=40 + sum(x[1] // 16 + 1 for x in lens), kind=kind,
+               cache=cache) as c:
+        attend_case(c, lens, 32, label="pieces")
+        attend_case(c, lens, 32, window=50, label="pieces")
+
+
 def test_a_nan_key_reaches_the_queries_that_see_it():
     """Alone in its stretch of keys, so that the wave or part that meets it has no other score."""
     for lens in ([(1, 257), (1, 1), (2, 1500)], [(70, 1025)]):
