@@ -60,6 +60,7 @@ int launch_remap(const RemapLaunch &a, hipStream_t stream);
 // tiles) 35 -> 42 us, sixteen of 200 to 5015 (10 tiles) 222 -> 213 us for four layers.
 #define KVX_ACROSS 10
 #define KVX_APPEND_TOKENS 8   // new tokens of one append item
+#define KVX_APPEND_SPLIT 4    // workgroups of one append item
 #define KVX_JOIN_ROWS 4       // rows joined by one workgroup
 
 // Rows of a piece of the many-rows kernel: 32 to a wave; at the widest heads a wave's
