@@ -344,7 +344,8 @@ KV_API int kv_pool_fork_blocks(kv_pool *pool, int64_t n_tokens, const int32_t *i
  * blocks with the src blocks' references, and each src block still, with one reference of
  * its own: the caller copies the pages (kv_copy_pages), rewrites the block tables on the
  * device (kv_remap_tables) and in its own memory, and, once nothing reads the old pages, frees the
- * src ids.  Host only. */
+ * src ids.  Until then no later plan moves a src block again, so a pool may be compacted a few
+ * pages at a time: plan, copy and rewrite, then the next plan.  Host only. */
 KV_API int kv_pool_plan_compact(kv_pool *pool, int32_t max_moves, kv_page_copy *moves, int32_t *n_moves);
 
 /* ---- calls -------------------------------------------------------------------- */

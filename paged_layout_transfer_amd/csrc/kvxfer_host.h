@@ -120,6 +120,7 @@ struct BlockBitmap {
         n_free = n;
         low_word = 0;
         free_bits.assign((size_t)((n + 63) / 64), ~0ull);
+        moving.assign(free_bits.size(), 0);
         if (n % 64) free_bits.back() = (1ull << (n % 64)) - 1;
     }
     bool is_free(int64_t id) const { return (free_bits[(size_t)(id >> 6)] >> (id & 63)) & 1u; }
@@ -166,10 +167,15 @@ struct BlockBitmap {
                 }
             }
             low_word = std::min<int64_t>(low_word, ids[i] >> 6);
+            moving[(size_t)(ids[i] >> 6)] &= ~(1ull << (ids[i] & 63));
             ++n_free;
         }
         return KV_OK;
     }
+
+    // Blocks that a compaction has moved and that are not free yet: a bitmap like free_bits.
+    // No later compaction moves them again.
+    std::vector<uint64_t> moving;
 
     // References of an allocated block beyond its first, held only for blocks that have
     // any.  Not bounded by a small type: 2^31 - 2 of them.
@@ -210,6 +216,9 @@ struct BlockBitmap {
         return rc;
     }
 
+    // The blocks of a word that a compaction does not move: free, or moved already.
+    uint64_t left_alone(int64_t word) const { return free_bits[(size_t)word] | moving[(size_t)word]; }
+
     // The moves of a compaction (kv_pool_plan_compact): the lowest free blocks take the
     // references of the highest allocated ones, which keep one.
     int32_t compact(int32_t max_moves, int32_t block_size, kv_page_copy *moves)
@@ -218,13 +227,14 @@ struct BlockBitmap {
         int32_t n = 0;
         for (; n < max_moves; ++n) {
             while (lo < hi && !is_free(lo)) lo += free_bits[(size_t)(lo >> 6)] ? 1 : 64 - (lo & 63);
-            while (hi > lo && is_free(hi)) hi -= ~free_bits[(size_t)(hi >> 6)] ? 1 : 1 + (hi & 63);
+            while (hi > lo && (left_alone(hi >> 6) >> (hi & 63) & 1u)) hi -= ~left_alone(hi >> 6) ? 1 : 1 + (hi & 63);
             if (lo >= hi) break;
             moves[n] = kv_page_copy{(int32_t)hi--, (int32_t)lo++, block_size};
         }
         for (int32_t i = 0; i < n; ++i) {
             const kv_page_copy &m = moves[i];
             free_bits[(size_t)(m.dst >> 6)] &= ~(1ull << (m.dst & 63));
+            moving[(size_t)(m.src >> 6)] |= 1ull << (m.src & 63);
             auto node = extra.extract(m.src);  // the node moves with its key: nothing is allocated
             if (!node.empty()) {
                 node.key() = m.dst;

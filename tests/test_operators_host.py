@@ -103,6 +103,47 @@ def test_compaction_pairs_highest_pages_with_lowest_holes(N, live, most):
     K.kv_pool_destroy(p)
 
 
+@pytest.mark.parametrize("N,most", [(16, 2), (200, 7), (300, 64)])
+def test_a_pool_is_compacted_a_few_pages_at_a_time(N, most):
+    """Plans made one after another, no source freed in between: every move is of another page."""
+    rng = np.random.default_rng(N)
+    p = _pool(N=N)
+    K.kv_pool_alloc_blocks(p, N)
+    gone = np.sort(rng.permutation(N)[:N // 2])
+    keep = np.setdiff1d(np.arange(N), gone)
+    K.kv_pool_free_blocks(p, gone)
+    K.kv_pool_share_blocks(p, keep[::2])
+    refs = {int(i): K.kv_pool_block_refs(p, int(i)) for i in keep}
+    where, moved = {i: i for i in refs}, []       # a page's place by its first one
+    have, holes = [int(i) for i in keep], [int(i) for i in gone]
+    while True:
+        want = []
+        while len(want) < most and have and holes and holes[0] < have[-1]:
+            want.append((have.pop(), holes.pop(0)))
+        moves = K.kv_pool_plan_compact(p, most)
+        got = [(m.src, m.dst) for m in moves[:moves._n]]
+        assert got == want[::-1]
+        if not got:
+            break
+        for src, dst in got:
+            assert where.pop(src) == src
+            where[dst] = src
+            moved.append(src)
+        assert K.kv_pool_free_count(p) == len(gone) - len(moved)
+    assert len(set(moved)) == len(moved) > most
+    assert all(K.kv_pool_block_refs(p, at) == refs[first] for at, first in where.items())
+    assert all(K.kv_pool_block_refs(p, i) == 1 for i in moved)
+    K.kv_pool_free_blocks(p, moved)
+    assert K.kv_pool_free_count(p) == len(gone)
+    # freed sources are ordinary blocks again: handed out and moved like any other
+    again = K.kv_pool_alloc_blocks(p, K.kv_pool_free_count(p))
+    assert set(moved) <= set(again.tolist())
+    K.kv_pool_free_blocks(p, [i for i in again if i != max(moved)])
+    moves = K.kv_pool_plan_compact(p, most)
+    assert [(m.src, m.dst) for m in moves[:moves._n]] == [(max(moved), len(keep))]
+    K.kv_pool_destroy(p)
+
+
 COPIES = [
     ([(0, 64, 1)], K.KV_ERR_RANGE), ([(-1, 2, 1)], K.KV_ERR_RANGE), ([(0, 1, 0)], K.KV_ERR_ARG),
     ([(0, 1, 17)], K.KV_ERR_ARG), ([(0, 1, 4), (2, 1, 4)], K.KV_ERR_DUP), ([(0, 1, 4), (1, 2, 4)], K.KV_ERR_DUP),
