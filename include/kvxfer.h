@@ -526,8 +526,10 @@ KV_API int kv_append_tokens(kv_attn_plan *plan, int32_t layer, const kv_append_a
  * new tokens must be in the cache already (kv_append_tokens on the same stream).  out may be q
  * itself, with its strides; it overlaps nothing else that the call reads.  A block id out of range is
  * reported (kv_pool_get_error) and block 0 read in its place: the result of the queries that
- * see it is undefined.  Errors: as kv_append_tokens; also KV_ERR_ARG for scale or softcap that are not
- * finite, softcap < 0, scale / softcap over the 32-bit range, or rows of out that overlap.
+ * see it is undefined.  A cap adds at most 2^-21 softcap to a score's error up to softcap 64, and beyond a few
+ * units in the last place of the score.  Errors: as kv_append_tokens; also KV_ERR_ARG for scale or softcap that
+ * are not finite, softcap < 0, scale * k_scale, softcap or scale * k_scale / softcap over the 32-bit range, or
+ * rows of out that overlap.
  * Captured, a call holds the kernels for any sequences within the plan's limits. */
 KV_API int kv_attend(kv_attn_plan *plan, int32_t layer, const kv_attend_args *args, hipStream_t stream);
 

@@ -238,14 +238,36 @@ __device__ __forceinline__ int64_t key_offset(const AttnLaunch &a, const Piece &
     return (int64_t)blk * a.block_stride + ((int64_t)slot * a.tok_stride + (int64_t)s.head * a.head_stride);
 }
 
-// Score transforms other than one positive scale: the tanh cap, the distance slopes, and
-// scales that are not positive.  Base-2 scores out.  key(i) is the key of score i.
-template <int N, class X, class Key>
+// Score transforms other than one positive scale, by the kernels' SHAPED: 1 the tanh cap, the distance slopes and
+// scales that are not positive; 2 a cap over KVX_CAP_SMALL, with slopes or without; 0 none of them, nothing to
+// do here.  Base-2 scores out.  key(i) is the key of score i.
+template <int SHAPED, int N, class X, class Key>
 __device__ __forceinline__ void shape(const AttnLaunch &a, X &x, float slope_log2, int32_t p, Key key)
 {
-    if (a.cap_log2 != 0.f) {
-        // c tanh y = c - 2 c / (e^2y + 1); the scale makes 2^x of it e^2y.  The reciprocal is good to
-        // one unit in the last place: 2^-23 of the cap.
+    if (SHAPED == 2) {
+        // c tanh(s / c) = s R((s / c)^2), R(u) = tanh(sqrt u) / sqrt u, relative to the score itself however
+        // large the cap is.  R is a minimax quotient of two polynomials on |s / c| <= KVX_CAP_EDGE, good to
+        // 2^-26.2; beyond, tanh is 1 - 2^-23.8 or more.  Coefficients and u are positive, so nothing
+        // cancels: 24 roundings of 2^-24 at most, 2^-21.4 of the score the worst of 4 million.  The bounds
+        // let NaN pass.
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float w = __builtin_elementwise_maximum(
+                __builtin_elementwise_minimum(x[i] * a.scale_log2, a.cap_edge), -a.cap_edge);
+            const float y = w * a.cap_inv, u = y * y;
+            float num = __builtin_fmaf(u, 1.40824019e-08f, 2.11223269e-05f);
+            float den = __builtin_fmaf(u, 8.07060701e-07f, 3.33626464e-04f);
+            num = __builtin_fmaf(u, num, 3.52639798e-03f);
+            den = __builtin_fmaf(u, den, 2.59938873e-02f);
+            num = __builtin_fmaf(u, num, 1.34068727e-01f);
+            den = __builtin_fmaf(u, den, 4.67401952e-01f);
+            num = __builtin_fmaf(u, num, 1.f);
+            den = __builtin_fmaf(u, den, 1.f);
+            x[i] = w * num * __builtin_amdgcn_rcpf(den);
+        }
+    } else if (a.cap_log2 != 0.f) {
+        // c tanh y = c - 2 c / (e^2y + 1); the scale makes 2^x of it e^2y.  A difference of numbers near the
+        // cap, good to 2^-21 of it: 3e-5 of a score at KVX_CAP_SMALL.
 #pragma unroll
         for (int i = 0; i < N; ++i)
             x[i] = __builtin_fmaf(-2.f * a.cap_log2, __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(x[i] * a.scale_log2) + 1.f),
@@ -321,7 +343,7 @@ __device__ __forceinline__ void store_lse(const AttnLaunch &a, int64_t row, int3
 // bf16 heads, 4 query heads to a cache head: 32 sequences of 1 K to 64 K tokens 306 us, 5.7 TB/s;
 // one of 32 K 28 us and 6 us to join; a context that one step of each wave covers 7 us, the latency of
 // record, block id, rows and the way out.
-template <class T, bool E4M3, int DP, bool SHAPED>
+template <class T, bool E4M3, int DP, int SHAPED>
 __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_few(const AttnLaunch a)
 {
     typedef typename Vec<T>::x8 T8;
@@ -465,7 +487,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_few(const AttnL
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             auto at = [&](int r) { return j0 + 16 * t + 4 * g + r; };
-            if (SHAPED) shape<4>(a, x[t], slope, pos, at);
+            if (SHAPED) shape<SHAPED, 4>(a, x[t], slope, pos, at);
             if (masked) hide<4>(x[t], mask, at);
         }
         float mx = fmaxf(fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[0][2], x[0][3])),
@@ -600,7 +622,7 @@ constexpr int many_lds() { return KVX_TILE_KEYS * (2 * (key_row<DP>() + value_ro
 // 128: 8192 tokens 565-585 us, 940-973 TFLOP/s; 2048 tokens on 34816 cached 1120-1157 us,
 // 980-1012; the clock falls to 2.0-2.2 GHz meanwhile.  Direct loads to shared memory make the
 // compiler wait for all of them before each read, and lost to the way through registers.
-template <class T, bool E4M3, int DP, bool SHAPED>
+template <class T, bool E4M3, int DP, int SHAPED>
 __global__ __launch_bounds__(64 * many_waves<DP>(), DP == 64 ? 4 : DP == 128 ? 2 : 1) void attend_many(const AttnLaunch a)
 {
     typedef typename Vec<T>::x8 T8;
@@ -730,7 +752,7 @@ __global__ __launch_bounds__(64 * many_waves<DP>(), DP == 64 ? 4 : DP == 128 ? 2
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             auto key = [&](int r) { return j0 + 32 * t + 8 * (r >> 2) + 4 * g + (r & 3); };
-            if (SHAPED) shape<16>(a, x[t], slope, pos, key);
+            if (SHAPED) shape<SHAPED, 16>(a, x[t], slope, pos, key);
             if (masked) hide<16>(x[t], mask, key);
         }
         float mx = x[0][0];
@@ -947,14 +969,18 @@ template <class T, bool E4M3, int DP>
 int launch_attend_dim(const AttnLaunch &a, int which, uint32_t grid, hipStream_t stream)
 {
     // one positive scale is folded into the exponential; anything else is shaped first
-    const bool plain = a.cap_log2 == 0.f && !a.slopes && a.scale_log2 > 0.f;
+    const bool plain = a.cap_log2 == 0.f && !a.slopes && a.scale_log2 > 0.f, large = a.cap_inv != 0.f;
     const void *fn;
     size_t lds = 0;
     uint32_t threads = 256;
     if (which == 0) {
-        fn = plain ? (const void *)&attend_few<T, E4M3, DP, false> : (const void *)&attend_few<T, E4M3, DP, true>;
+        fn = plain   ? (const void *)&attend_few<T, E4M3, DP, 0>
+             : large ? (const void *)&attend_few<T, E4M3, DP, 2>
+                     : (const void *)&attend_few<T, E4M3, DP, 1>;
     } else {
-        fn = plain ? (const void *)&attend_many<T, E4M3, DP, false> : (const void *)&attend_many<T, E4M3, DP, true>;
+        fn = plain   ? (const void *)&attend_many<T, E4M3, DP, 0>
+             : large ? (const void *)&attend_many<T, E4M3, DP, 2>
+                     : (const void *)&attend_many<T, E4M3, DP, 1>;
         lds = many_lds<DP>();
         threads = 64 * many_waves<DP>();
         const hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);

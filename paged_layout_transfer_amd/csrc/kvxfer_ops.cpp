@@ -6,6 +6,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <limits>
 #include <new>
 #include <vector>
 
@@ -481,9 +482,15 @@ int kv_attend(kv_attn_plan *p, int32_t layer, const kv_attend_args *x, hipStream
     a.q_head = x->q_head_stride;
     a.out_token = x->out_token_stride;
     a.out_head = x->out_head_stride;
-    a.scale_log2 = (float)((x->softcap > 0 ? 2 / (double)x->softcap : 1.0) * scale * log2e);
+    const bool small = x->softcap > 0 && x->softcap <= KVX_CAP_SMALL;
+    a.scale_log2 = (float)((small ? 2 / (double)x->softcap : 1.0) * scale * log2e);
     a.cap_log2 = (float)(x->softcap * log2e);
-    if (!std::isfinite(a.scale_log2) || !std::isfinite(2 * a.cap_log2)) return KV_ERR_ARG;
+    if (!std::isfinite(a.scale_log2) || !std::isfinite(a.cap_log2)) return KV_ERR_ARG;
+    if (x->softcap > KVX_CAP_SMALL) {
+        const double cap = x->softcap * log2e;
+        a.cap_inv = (float)(1 / cap);
+        a.cap_edge = (float)std::min(KVX_CAP_EDGE * cap, (double)std::numeric_limits<float>::max());
+    }
     a.v_scale = e4m3 ? x->v_scale : 1.f;
     // a captured call holds every kernel that a plan within the limits may need
     for (int which = 0; which < 2; ++which) {

@@ -1,0 +1,104 @@
+"""Attention over its arguments' whole range, on the GPU against 64 bits: caps far above the scores,
+tails far below the largest score, infinite and NaN values at every padded width."""
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+import paged_reference as ref
+from paged_layout_transfer_amd import kvxfer as K
+from test_gpu_operators import Cache, deal, say, seqs_of
+
+pytestmark = pytest.mark.gpu
+
+F = 2.0 ** -24      # half a unit in the last place of 32 bits
+
+
+def run(c, lens, heads_q, q, **kw):
+    """out and lse of one call, on the host in 64 bits, with each sequence's rows and cache."""
+    tables = deal(c, lens)
+    on_gpu = [t.cuda() for t in tables]
+    seqs, rows = seqs_of(on_gpu, lens)
+    plan = c.plan(heads_q, len(lens), rows, kw.pop("window", 0))
+    K.kv_attn_plan_set(plan, K.make_seqs(seqs))
+    qd = q.cuda()
+    out, lse = torch.zeros_like(qd), torch.zeros(rows, heads_q, device="cuda")
+    K.kv_attend(plan, 0, K.make_attend_args(qd, out, lse, n_tokens=rows, k_scale=c.k_scale, v_scale=c.v_scale, **kw))
+    torch.cuda.synchronize()
+    held = [(at, q_len, *(ref.cache_of(c.region(0, i), False, t, n) for i in (0, 1)))
+            for t, (_, _, n, at, q_len, _) in zip(tables, seqs)]
+    return out.cpu().double(), lse.cpu().double(), held
+
+
+CAPS = [0.5, 30.0, 64.0, 65.0, 1e3, 1e4, 1e5, 1e6, 1e7, 1e20, 2e38]
+
+
+@pytest.mark.parametrize("softcap", CAPS)
+@pytest.mark.parametrize("lens", [[(1, 700), (3, 90)], [(70, 400)]], ids=["few", "many"])
+@pytest.mark.parametrize("kind,held,dim", [("f16", "f16", 64), ("bf16", "e4m3", 128)])
+def test_a_cap_is_exact_however_large(softcap, lens, kind, held, dim):
+    """The bound is relative to the score for caps over 64, 2^-21 of the cap below.  With f = 2^-24: the products' sum as in
+    paged_reference.attend, f (dim + 8) scale sum|q k|, which a cap only shrinks; then of c tanh(s / c)
+    = s P(u) / Q(u), u = (s / c)^2, at most 24 roundings: scale and base 2, s / c 3 (u twice that and its
+    own, worth half in the quotient, 4), P and Q 5 each with their coefficients, reciprocal 2, two
+    products 2, the quotient's own error and the edge's 2 (2^-23.8 and 2^-26.2).  A weight is off by twice the
+    worst error of a score, as is their sum."""
+    with Cache(heads=2, dim=dim, page=16, blocks=60, kind=kind, cache=held) as c:
+        gen = torch.Generator().manual_seed(7)
+        rows = sum(x[0] for x in lens)
+        # scores of standard deviation 3 to 4
+        q = (torch.randn((rows, 4, dim), generator=gen) * 3).to(ref.TYPES[kind])
+        scale = 1 / math.sqrt(dim)
+        say("cap", softcap, lens, kind, held, dim)
+        out, lse, seqs = run(c, lens, 4, q, scale=scale, softcap=softcap)
+        u = torch.finfo(ref.TYPES[kind]).eps / 2
+        ks, vs = (float(torch.tensor(x, dtype=torch.float32)) for x in (c.k_scale, c.v_scale))
+        for at, n_q, k, v in seqs:
+            n = k.shape[0]
+            seen = ref.visible(n_q, n)
+            for x in range(4):
+                qq, kk, vv = q[at:at + n_q, x].double(), k[:, x // 2] * ks, v[:, x // 2] * vs
+                s = softcap * torch.tanh(qq @ kk.t() * scale / softcap)
+                ds = F * (dim + 8) * scale * (qq.abs() @ kk.abs().t())
+                ds = ds + (24 * F * s.abs() if softcap > 64 else 8 * F * s.abs() + 2.0 ** -21 * softcap)
+                e = torch.where(seen, ds, 0.0).amax(-1)
+                s = torch.where(seen, s, -math.inf)
+                z = torch.logsumexp(s, -1)
+                w = torch.exp(s - z[:, None])
+                want, a = w @ vv, w @ vv.abs()
+                rel = (2 * e + (4 * n + 64) * F)[:, None]
+                small = 2.0 ** -25 * (seen.double() @ vv.abs()) if kind == "f16" else 0.0
+                tol = a * (u + rel) + small + want.abs() * (u + rel) + torch.finfo(ref.TYPES[kind]).smallest_normal * 2 * u
+                got, got_z = out[at:at + n_q, x], lse[at:at + n_q, x]
+                off = (got - want).abs() / tol
+                assert off.max() <= 1, "out: %g of what is allowed" % off.max()
+                off = (got_z - z).abs() / (e + (4 * n + 64) * F + 8 * F * z.abs())
+                assert off.max() <= 1, "lse: %g of what is allowed" % off.max()
+
+
+@pytest.mark.parametrize("lens", [[(1, 40)], [(40, 80)]], ids=["few", "many"])
+def test_a_capped_score_that_is_infinite_or_nan(lens):
+    """An infinite score is at the cap; NaN stays NaN."""
+    with Cache(heads=1, dim=64, page=16, blocks=20, kind="bf16") as c:
+        for t, (_, n) in zip(deal(c, lens), lens):
+            at = lambda j: c.host[0][int(t[j // 16]), j % 16, 0]       # noqa: E731
+            at(3)[0] = math.inf
+            at(7)[0] = -math.inf
+            at(n - 1)[1] = math.nan
+        c.upload()
+        rows = lens[0][0]
+        q = torch.rand(rows, 1, 64, generator=torch.Generator().manual_seed(1)).bfloat16() + 0.1
+        say("infinite capped scores", lens)
+        out, lse, seqs = run(c, lens, 1, q, scale=0.125, softcap=5.0)
+        (_, n_q, k, v), = seqs
+        s = 5 * torch.tanh(q[:, 0].double() @ k[:, 0].t() * 0.125 / 5)
+        assert (s[:, 3] == 5).all() and (s[:, 7] == -5).all()
+        s = torch.where(ref.visible(n_q, k.shape[0]), s, -math.inf)
+        z = torch.logsumexp(s, -1)
+        assert torch.equal(torch.isnan(lse[:, 0]), torch.isnan(z)) and torch.isnan(z[-1])
+        assert torch.equal(torch.isnan(out[:, 0]), torch.isnan(z)[:, None].expand(-1, 64))
+        fine = ~torch.isnan(z)
+        # scores below 5: their products' sums 72 roundings of at most 20, the cap 24 of 5; the sum 4 n + 64
+        assert ((lse[:, 0] - z).abs()[fine] <= F * (72 * 20 + 24 * 5 + 4 * 80 + 64 + 64)).all()
