@@ -102,3 +102,43 @@ def test_a_capped_score_that_is_infinite_or_nan(lens):
         fine = ~torch.isnan(z)
         # scores below 5: their products' sums 72 roundings of at most 20, the cap 24 of 5; the sum 4 n + 64
         assert ((lse[:, 0] - z).abs()[fine] <= F * (72 * 20 + 24 * 5 + 4 * 80 + 64 + 64)).all()
+
+
+@pytest.mark.parametrize("lens", [[(1, 700)], [(2, 9000), (1, 5000)], [(40, 5000)], [(66, 3000)] * 12],
+                         ids=["few", "few_cut", "many", "many_whole"])
+@pytest.mark.parametrize("kind,held,dim", [("f16", "f16", 64), ("f16", "f16", 256), ("f16", "e4m3", 128), ("bf16", "bf16", 64)])
+def test_a_long_tail_far_below_the_first_key(lens, kind, held, dim):
+    """The first key's score lies 17.5 above the others', which hold all of the values (none is negative, so
+    the sum of absolute values is the result).  The bounds are those of paged_reference.attend, one product a
+    score, but half weights lose 2^-32 of the largest one: they are scaled by 2^7, and the largest is at
+    least 1 before that."""
+    heads = 2
+    with Cache(heads=heads, dim=dim, page=16, blocks=sum(n // 16 + 1 for _, n in lens), kind=kind, cache=held) as c:
+        c.k_scale = c.v_scale = 1.0
+        gen = torch.Generator().manual_seed(9)
+        c.host[0] = 0
+        c.host[0][..., 0] = (torch.rand(c.host[0].shape[:-1], generator=gen) * 2 - 1).to(c.host.dtype)
+        c.host[1] = (torch.rand(c.host[1].shape, generator=gen) * 8 + 8).to(c.host.dtype)
+        for t in deal(c, lens):
+            c.host[0][int(t[0]), 0, :, 0] = torch.tensor(17.5).to(c.host.dtype)      # 18 in e4m3
+            c.host[1][int(t[0]), 0] = 0
+        c.upload()
+        rows = sum(x[0] for x in lens)
+        q = torch.zeros(rows, 4 * heads, dim)
+        q[..., 0] = 8
+        q = q.to(ref.TYPES[kind])
+        say("long tail", lens[:3], kind, held, dim)
+        out, lse, seqs = run(c, lens, 4 * heads, q, scale=0.125)
+        u = torch.finfo(ref.TYPES[kind]).eps / 2
+        for at, n_q, k, v in seqs:
+            want, z, _, tol_z = ref.attend(q[at:at + n_q].double(), k, v, scale=0.125, kind=kind)
+            n = k.shape[0]
+            e = F * (dim + 16) * 18
+            tol = 2 * want * (u + 2 * e + (4 * n + 64) * F) + torch.finfo(ref.TYPES[kind]).smallest_normal * 2 * u
+            if kind == "f16":
+                seen = ref.visible(n_q, n).double()
+                tol = tol + 2.0 ** -32 * torch.stack([seen @ v[:, x // 4] for x in range(4 * heads)], 1)
+            off = (out[at:at + n_q] - want).abs() / tol
+            assert off.max() <= 1, "out: %g of what is allowed, %g for %g" % (off.max(), out[at:at + n_q].flatten()[off.argmax()], want.flatten()[off.argmax()])
+            off = (lse[at:at + n_q] - z).abs() / tol_z
+            assert off.max() <= 1, "lse: %g of what is allowed" % off.max()
