@@ -521,7 +521,8 @@ KV_API int kv_append_tokens(kv_attn_plan *plan, int32_t layer, const kv_append_a
  * lse = -infinity.  Cached tokens that a query does not see do not reach its result, whatever
  * they hold (infinities and NaN too); pages that no query sees are not read and their table entries
  * may be anything.  Sums, maxima and both products' sums are held in 32 bits; the weights are rounded to
- * q_type for the second product (half weights below 2^-32 of the largest to zero).  Rows of no sequence are left as they were.  The same call
+ * q_type for the second product (half weights below 2^-32 of the largest to zero; infinite
+ * and NaN values that a query sees reach it all the same).  Rows of no sequence are left as they were.  The same call
  * gives the same bits: no atomics take part, and split sums are joined in a fixed order.  The
  * new tokens must be in the cache already (kv_append_tokens on the same stream).  out may be q
  * itself, with its strides; it overlaps nothing else that the call reads.  A block id out of range is

@@ -131,6 +131,40 @@ __device__ __forceinline__ typename Vec<T>::x8 ones_at(typename Vec<T>::x8 v, in
 }
 __device__ __forceinline__ float special(int kind) { return kind == 0 ? __builtin_nanf("") : kind == 1 ? INFINITY : -INFINITY; }
 
+// A seen infinity whose weight is zero (2^-149 of the largest, 2^-32 in half) has made NaN of a result that is
+// infinite.  Such results are set to zero, what they see of infinities and NaN is added, and those to which
+// nothing was added stay NaN: they are none of ours.
+template <class V, int N>
+struct Lost {
+    static constexpr int kEach = sizeof(V) / 4;
+    uint32_t bits[(N * kEach + 31) / 32] = {};
+    __device__ __forceinline__ void clear(V (&o)[N])
+    {
+#pragma unroll
+        for (int i = 0; i < N * kEach; ++i) {
+            const float x = o[i / kEach][i % kEach];
+            bits[i / 32] |= (x != x ? 1u : 0u) << (i % 32);
+            o[i / kEach][i % kEach] = x != x ? 0.f : x;
+        }
+    }
+    __device__ __forceinline__ void restore(V (&o)[N])
+    {
+#pragma unroll
+        for (int i = 0; i < N * kEach; ++i) {
+            const float x = o[i / kEach][i % kEach];
+            o[i / kEach][i % kEach] = (bits[i / 32] >> (i % 32) & 1u) && x == 0.f ? __builtin_nanf("") : x;
+        }
+    }
+    // Whether any result is infinite or NaN.
+    static __device__ __forceinline__ bool any(const V (&o)[N])
+    {
+        float x = 0.f;
+#pragma unroll
+        for (int i = 0; i < N * kEach; ++i) x = __builtin_fmaf(o[i / kEach][i % kEach], 0.f, x);
+        return x != x;
+    }
+};
+
 // Rows of a tile in shared memory, in values.  Key rows are one 16-byte chunk longer than
 // their values, so that the 16 lanes that read one chunk of 16 rows meet all banks; value rows 64
 // bytes, so that the transposing reads' 64-byte stretches of four rows do.  (Exchanging chunks
@@ -415,6 +449,44 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_few(const AttnL
                 }
         }
     };
+    auto put_values = [&]() __attribute__((always_inline)) {  // to shared memory, row-major
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int c = 0; c < kLoads; ++c) {
+                T *to = tile + (16 * t + n) * kRow + c * 4 * kVals + g * kVals;
+                if constexpr (E4M3) {
+                    const T4 w0 = from_e4m3<T>(vr[t][c][0]), w1 = from_e4m3<T>(vr[t][c][1]);
+                    const T4 w2 = from_e4m3<T>(vr[t][c][2]), w3 = from_e4m3<T>(vr[t][c][3]);
+                    *(T8 *)to = __builtin_shufflevector(w0, w1, 0, 1, 2, 3, 4, 5, 6, 7);
+                    *(T8 *)(to + 8) = __builtin_shufflevector(w2, w3, 0, 1, 2, 3, 4, 5, 6, 7);
+                } else {
+                    *(u32x4 *)to = vr[t][c];
+                }
+            }
+    };
+    // O^T: column d of keys 16 t + 4 g + r
+    const T *const col = tile + (4 * g + (n >> 2)) * kRow + (n & 3) * 4;
+    auto value = [&](int d) __attribute__((always_inline)) {
+        const T4 lo = read_column<T>(col + 16 * d), hi = read_column<T>(col + 16 * kRow + 16 * d);
+        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+    // Infinities and NaN among the values of the step from key j0 on, added where they are seen: where a product
+    // of ones, for seen keys and such values, is not zero.
+    auto seen_ones = [&](int32_t j0) __attribute__((always_inline)) {
+        T8 seen;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) seen[k] = (T)(mask.sees(j0 + 16 * (k >> 2) + 4 * g + (k & 3)) ? 1.f : 0.f);
+        return seen;
+    };
+    auto add_specials = [&](f32x4 &to, T8 v, T8 seen) __attribute__((always_inline)) {
+#pragma unroll
+        for (int kind = 0; kind < 3; ++kind) {
+            const f32x4 c = mfma16(ones_at<T>(v, kind), seen, f32x4{0, 0, 0, 0});
+#pragma unroll
+            for (int r = 0; r < 4; ++r) to[r] += c[r] != 0.f ? special(kind) : 0.f;
+        }
+    };
     int64_t off[2] = {0, 0};
     int32_t blk[2] = {0, 0};
     if (i < i1) {
@@ -466,21 +538,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_few(const AttnL
             }
         }
         if (more) load(kr, a.k_base, off);
-        // V to shared memory, row-major
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int c = 0; c < kLoads; ++c) {
-                T *to = tile + (16 * t + n) * kRow + c * 4 * kVals + g * kVals;
-                if constexpr (E4M3) {
-                    const T4 w0 = from_e4m3<T>(vr[t][c][0]), w1 = from_e4m3<T>(vr[t][c][1]);
-                    const T4 w2 = from_e4m3<T>(vr[t][c][2]), w3 = from_e4m3<T>(vr[t][c][3]);
-                    *(T8 *)to = __builtin_shufflevector(w0, w1, 0, 1, 2, 3, 4, 5, 6, 7);
-                    *(T8 *)(to + 8) = __builtin_shufflevector(w2, w3, 0, 1, 2, 3, 4, 5, 6, 7);
-                } else {
-                    *(u32x4 *)to = vr[t][c];
-                }
-            }
+        put_values();
         if (more) load(vr, a.v_base, off);
         if (i + 2 * apart < i1) {
 #pragma unroll
@@ -519,12 +577,6 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_few(const AttnL
                 l += e;
                 w[4 * t + r] = (T)e;
             }
-        // O^T: column d of keys 16 t + 4 g + r
-        const T *col = tile + (4 * g + (n >> 2)) * kRow + (n & 3) * 4;
-        auto value = [&](int d) {
-            const T4 lo = read_column<T>(col + 16 * d), hi = read_column<T>(col + 16 * kRow + 16 * d);
-            return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-        };
         bool odd = false;
         if (masked) {
 #pragma unroll
@@ -532,22 +584,13 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_few(const AttnL
         }
         if (masked && __any(odd)) {
             // An infinity or NaN among the values: a zero weight would turn it into NaN in rows
-            // that do not see it.  So it is left out of the product, and added where it is seen: where
-            // a product of ones, for seen keys and such values, is not zero.
-            T8 seen;
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                seen[k] = (T)(mask.sees(j0 + 16 * (k >> 2) + 4 * g + (k & 3)) ? 1.f : 0.f);
+            // that do not see it.  So it is left out of the product, and added where it is seen.
+            const T8 seen = seen_ones(j0);
 #pragma unroll
             for (int d = 0; d < DP / 16; ++d) {
                 const T8 v = value(d);
                 o[d] = mfma16(only_finite<T>(v), w, o[d]);
-#pragma unroll
-                for (int kind = 0; kind < 3; ++kind) {
-                    const f32x4 c = mfma16(ones_at<T>(v, kind), seen, f32x4{0, 0, 0, 0});
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) o[d][r] += c[r] != 0.f ? special(kind) : 0.f;
-                }
+                add_specials(o[d], v, seen);
             }
         } else {
 #pragma unroll
@@ -556,6 +599,22 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_few(const AttnL
     }
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
+    typedef Lost<f32x4, DP / 16> Results;
+    if (__builtin_expect(__any(Results::any(o) && l == l), 0)) {
+        Results lost;
+        lost.clear(o);
+        for (i = s.tile0 * 2 + first; i < i1; i += apart) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) off[t] = key_offset(a, s, key(i, t), block_of(a, s, key(i, t)));
+            load(vr, a.v_base, off);
+            put_values();
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            const T8 seen = seen_ones(start(i));
+#pragma unroll
+            for (int d = 0; d < DP / 16; ++d) add_specials(o[d], value(d), seen);
+        }
+        lost.restore(o);
+    }
 
     // join the four waves: their slices hold 16 rows of 32-bit results.  With a head to each wave
     // there is nothing to join, and a wave reads its own slice back, a row at a time.
@@ -802,6 +861,24 @@ __global__ __launch_bounds__(64 * many_waves<DP>(), DP == 64 ? 4 : DP == 128 ? 2
                 o[d] = mfma32(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7), w[u], o[d]);
             }
     };
+    // Infinities and NaN among the values of the tile `was` from key j0 on, added where they are seen.
+    auto add_specials = [&](const T *was, int32_t j0) __attribute__((always_inline)) {
+#pragma unroll 1
+        for (int k = 0; k < N; ++k) {
+            const bool seen = mask.sees(j0 + k);
+#pragma unroll
+            for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    const T4 v = *(const T4 *)(was + k * kV + 32 * d + 8 * b + 4 * g);
+                    // the whole vector: a bit cast of one element reads element 0
+                    const u16x4 bits = __builtin_bit_cast(u16x4, v);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        o[d][4 * b + e] += seen && not_finite<T>(bits[e]) ? (float)v[e] : 0.f;
+                }
+        }
+    };
     // Infinities and NaN among the values of a tile that some rows see in part: a zero weight would
     // turn them into NaN in rows that do not see them.  Before tile i is worked on it is read
     // again; its copy for the product gets zeros in their place, and each row adds those it sees from
@@ -819,23 +896,7 @@ __global__ __launch_bounds__(64 * many_waves<DP>(), DP == 64 ? 4 : DP == 128 ? 2
             *(T8 *)(V + (krow + c * kApart) * kV + chunk * 8) = only_finite<T>(v);
         }
         __syncthreads();
-        if (decltype(rows)::value) {
-#pragma unroll 1
-            for (int k = 0; k < N; ++k) {
-                const bool seen = mask.sees(start(i) + k);
-#pragma unroll
-                for (int d = 0; d < DP / 32; ++d)
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        const T4 v = *(const T4 *)(was + k * kV + 32 * d + 8 * b + 4 * g);
-                        // the whole vector: a bit cast of one element reads element 0
-                        const u16x4 bits = __builtin_bit_cast(u16x4, v);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            o[d][4 * b + e] += seen && not_finite<T>(bits[e]) ? (float)v[e] : 0.f;
-                    }
-            }
-        }
+        if (decltype(rows)::value) add_specials(was, start(i));
         __syncthreads();
     };
 
@@ -855,23 +916,41 @@ __global__ __launch_bounds__(64 * many_waves<DP>(), DP == 64 ? 4 : DP == 128 ? 2
         }
     }
     __syncthreads();
-    if (wave * 32 >= s.rows) {  // a wave without rows only helps loading
+    const bool works = wave * 32 < s.rows;  // a wave without rows only helps loading
+    if (!works) {
         for (int32_t i = 0; i < n_tiles; ++i) {
             if (__builtin_expect(odd[i & 1] == i + 1, 0)) specials(i, std::false_type{});
             stage(i);
             __syncthreads();
         }
-        return;
-    }
-    for (int32_t i = 0; i < n_tiles; ++i) {
-        if (__builtin_expect(odd[i & 1] == i + 1, 0)) specials(i, std::true_type{});
-        stage(i);
-        scores(i);
-        weights(start(i), partly(i));
-        add_values(i);
-        __syncthreads();
+    } else {
+        for (int32_t i = 0; i < n_tiles; ++i) {
+            if (__builtin_expect(odd[i & 1] == i + 1, 0)) specials(i, std::true_type{});
+            stage(i);
+            scores(i);
+            weights(start(i), partly(i));
+            add_values(i);
+            __syncthreads();
+        }
     }
     l += __shfl_xor(l, 32);
+    typedef Lost<f32x16, DP / 32> Results;
+    if (works && __any(Results::any(o) && l == l)) odd[0] = -1;
+    __syncthreads();
+    if (__builtin_expect(odd[0] == -1, 0)) {
+        Results lost;
+        if (works) lost.clear(o);
+        for (int32_t i = 0; i < n_tiles; ++i) {
+            if (wave == 0) place(i, find(i));
+            __syncthreads();
+            load(vr, a.v_base, i);
+#pragma unroll
+            for (int c = 0; c < kLoads; ++c) *(T8 *)(values + (krow + c * kApart) * kV + chunk * 8) = widen(vr[c]);
+            __syncthreads();
+            if (works) add_specials(values, start(i));
+        }
+        if (works) lost.restore(o);
+    }
     if (rw >= s.rows) return;
     const int64_t to_row = (int64_t)s.q_begin + tok;
     const float top = m == -INFINITY ? m : m * sc - weight_shift<T>();

@@ -142,3 +142,44 @@ def test_a_long_tail_far_below_the_first_key(lens, kind, held, dim):
             assert off.max() <= 1, "out: %g of what is allowed, %g for %g" % (off.max(), out[at:at + n_q].flatten()[off.argmax()], want.flatten()[off.argmax()])
             off = (lse[at:at + n_q] - z).abs() / tol_z
             assert off.max() <= 1, "lse: %g of what is allowed" % off.max()
+
+
+@pytest.mark.parametrize("lens", [[(1, 300), (3, 900)], [(1, 9000)], [(70, 600), (40, 2000)], [(66, 700)] * 20],
+                         ids=["few", "few_cut", "many", "many_whole"])
+@pytest.mark.parametrize("kind,held,dim,apart", [("f16", "f16", 64, 40), ("bf16", "bf16", 128, 40), ("bf16", "bf16", 64, 200),
+                                                 ("f16", "f16", 256, 200), ("f16", "e4m3", 128, 40), ("bf16", "bf16", 80, 200)])
+def test_a_seen_infinity_counts_however_small_its_weight(lens, kind, held, dim, apart):
+    """Infinite and NaN values of keys whose scores lie `apart` below those of every 32nd key, which come before
+    them in whatever order the keys are taken: their weights are small, or zero in 32 bits, but positive.  In
+    stretches of keys that every query sees, and nothing of it reaches the other columns and heads."""
+    heads = 2
+    with Cache(heads=heads, dim=dim, page=16, blocks=sum(n // 16 + 1 for _, n in lens), kind=kind, cache=held) as c:
+        c.host[0] = 0
+        for t, (q, n) in zip(deal(c, lens), lens):
+            for j in range(0, n, 32):
+                c.host[0][int(t[j // 16]), j % 16, :, 0] = torch.tensor(16.0).to(c.host.dtype)
+            at = lambda j: c.host[1][int(t[j // 16]), j % 16]       # noqa: E731
+            at(0)[0, 3] = math.nan
+            if held != "e4m3":
+                at(1)[0, 5] = math.inf
+                at(70)[1, 9] = -math.inf
+                at(5)[1, dim - 1], at(100)[1, dim - 1] = math.inf, math.inf
+                at(6)[0, 11], at(130)[0, 11] = math.inf, -math.inf
+        c.upload()
+        rows = sum(x[0] for x in lens)
+        q = torch.zeros(rows, 4 * heads, dim)
+        q[..., 0] = apart / 16 / c.k_scale
+        q = q.to(ref.TYPES[kind])
+        say("infinities of small weight", lens[:3], kind, held, dim, apart)
+        out, lse, seqs = run(c, lens, 4 * heads, q, scale=1.0)
+        assert torch.isfinite(lse).all()
+        ks, vs = (float(torch.tensor(x, dtype=torch.float32)) for x in (c.k_scale, c.v_scale))
+        for at, n_q, k, v in seqs:
+            want, _, tol, _ = ref.attend(q[at:at + n_q].double(), k, v, scale=1.0, kind=kind, k_scale=ks, v_scale=vs)
+            got = out[at:at + n_q]
+            assert torch.equal(torch.isnan(got), torch.isnan(want)) and torch.isnan(got).any()
+            inf = torch.isinf(want)
+            assert torch.equal(torch.isinf(got), inf) and torch.equal(got[inf], want[inf])
+            assert inf.any() or held == "e4m3"
+            fin = torch.isfinite(want)
+            assert ((got - want).abs()[fin] <= tol[fin]).all()
