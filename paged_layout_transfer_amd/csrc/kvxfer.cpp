@@ -352,12 +352,15 @@ int device_setup(kv_pool *p)
     if (!HIP_OK(hipGetDevice(&dev))) return KV_ERR_HIP;
     if (p->device >= 0) return dev == p->device ? KV_OK : KV_ERR_ARG;
     const int64_t n = (int64_t)p->desc.num_layers * p->desc.num_kv;
+    const int32_t no_error = 0;
 
     if (!HIP_OK(hipMalloc(&p->d_regions, n * sizeof(void *)))) goto fail;
     if (!HIP_OK(hipMemcpy(p->d_regions, p->bases.data(), n * sizeof(void *), hipMemcpyHostToDevice)))
         goto fail;
     if (!HIP_OK(hipMalloc(&p->d_err, sizeof(int32_t)))) goto fail;
-    if (!HIP_OK(hipMemset(p->d_err, 0, sizeof(int32_t)))) goto fail;
+    // a copy that the host waits for: a clear left on the null stream could fall behind the first
+    // kernel, on another stream, and take its error away
+    if (!HIP_OK(hipMemcpy(p->d_err, &no_error, sizeof(int32_t), hipMemcpyHostToDevice))) goto fail;
     if (!HIP_OK(hipMalloc(&p->d_arena, kArenaBytes))) goto fail;
     if (!HIP_OK(hipHostMalloc((void **)&p->h_arena, kArenaBytes, hipHostMallocDefault))) goto fail;
     p->arena.reset();

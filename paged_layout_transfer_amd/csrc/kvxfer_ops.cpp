@@ -339,6 +339,8 @@ int kv_attn_plan_create(kv_pool *pool, const kv_attn_desc *desc, kv_attn_plan **
         for (int i = 0; ok && i < 2; ++i)
             ok = HIP_OK(hipHostMalloc((void **)&p->host[i], p->bytes, hipHostMallocDefault)) &&
                  HIP_OK(hipEventCreateWithFlags(&p->sent[i], hipEventDisableTiming));
+        // the zeros are on the null stream: a plan set on another must not run before them
+        ok = ok && HIP_OK(hipDeviceSynchronize());
         if (!ok) rc = KV_ERR_HIP;
     }
     if (rc) {

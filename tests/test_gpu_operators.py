@@ -773,3 +773,28 @@ def test_a_pool_destroyed_behind_its_page_copies():
     assert side.query()
     want[32:40] = want[:8]
     assert torch.equal(region, want) and table[:8].tolist() == list(range(32, 40)) and table[8:].tolist() == list(range(8, 64))
+
+
+def test_a_plan_is_ready_on_every_stream_when_create_returns():
+    """Made behind work on the null stream, set and used on another at once."""
+    with Cache(heads=2, dim=64, page=16, blocks=64, kind="bf16") as c:
+        lens = [(1, 300), (2, 90)]
+        tables = [t.cuda() for t in deal(c, lens)]
+        seqs, rows = seqs_of(tables, lens)
+        q = torch.randn(rows, 4, 64, device="cuda").bfloat16()
+        out, want = torch.zeros_like(q), torch.zeros_like(q)
+        args = [K.make_attend_args(q, o, n_tokens=rows, scale=0.125) for o in (out, want)]
+        plan = c.plan(4, 2, rows)
+        K.kv_attn_plan_set(plan, K.make_seqs(seqs))
+        K.kv_attend(plan, 0, args[1])
+        side, big = torch.cuda.Stream(), torch.ones(1 << 28, device="cuda")
+        torch.cuda.synchronize()
+        say("a plan made behind other work")
+        for _ in range(60):
+            big.mul_(1.0)
+        plan = c.plan(4, 2, rows)
+        assert torch.cuda.current_stream().query()      # the header's promise: it waits for the device
+        K.kv_attn_plan_set(plan, K.make_seqs(seqs), side)
+        K.kv_attend(plan, 0, args[0], side)
+        torch.cuda.synchronize()
+        assert (want != 0).any() and torch.equal(words(out), words(want))
