@@ -932,7 +932,9 @@ int kv_pool_get_error(kv_pool *p, hipStream_t stream, int32_t *out_bits)
     if (!HIP_OK(hipStreamSynchronize(stream))) return KV_ERR_HIP;
     int32_t v = 0;
     if (!HIP_OK(hipMemcpy(&v, p->d_err, sizeof(v), hipMemcpyDeviceToHost))) return KV_ERR_HIP;
-    if (v && !HIP_OK(hipMemset(p->d_err, 0, sizeof(int32_t)))) return KV_ERR_HIP;
+    // cleared by the time the call returns: the next kernel's error, on whatever stream, stays
+    const int32_t no_error = 0;
+    if (v && !HIP_OK(hipMemcpy(p->d_err, &no_error, sizeof(v), hipMemcpyHostToDevice))) return KV_ERR_HIP;
     *out_bits = v;
     return v ? KV_ERR_DEVICE : KV_OK;
 }

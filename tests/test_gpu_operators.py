@@ -798,3 +798,22 @@ def test_a_plan_is_ready_on_every_stream_when_create_returns():
         K.kv_attend(plan, 0, args[0], side)
         torch.cuda.synchronize()
         assert (want != 0).any() and torch.equal(words(out), words(want))
+
+
+def test_an_error_right_after_the_last_one_was_read_is_not_lost():
+    """Reading clears the error word before it returns: calls on a stream of their own, behind work on
+    the null stream that waits for none of them."""
+    with Cache(heads=2, dim=64, page=16, blocks=64, kind="bf16") as c:
+        side = torch.cuda.Stream()
+        table = torch.full((20,), 64, dtype=torch.int32, device="cuda")
+        q = torch.randn(1, 4, 64, device="cuda").bfloat16()
+        out, big = torch.zeros_like(q), torch.ones(1 << 22, device="cuda")
+        plan = c.plan(4, 1, 1)
+        K.kv_attn_plan_set(plan, K.make_seqs([(table, 20, 300, 0, 1)]), side)
+        args = K.make_attend_args(q, out, n_tokens=1, scale=0.125)
+        say("errors one after another")
+        for _ in range(100):
+            K.kv_attend(plan, 0, args, side)
+            big.mul_(1.0)
+            assert K.kv_pool_get_error(c.handle, side) == K.KV_DEVERR_BLOCK_RANGE
+        assert K.kv_pool_get_error(c.handle, side) == 0
