@@ -301,9 +301,10 @@ KV_API int kv_pool_create(const kv_pool_desc *desc, kv_pool **out);
 /* Frees the handle and its device state, after waiting for the transfers it
  * queued that are still in flight (their fence events; other device work is not
  * waited for, unless the pool has copied pages or rewritten tables: then the device is idle
- * first; nor are replays of calls captured into graphs: those must have finished,
- * and such graphs must not run again).  The caller's regions are untouched.  NULL is
- * accepted.
+ * first, and where that cannot be waited for because a stream captures, which the attempt ends, the
+ * call returns KV_ERR_HIP and the pool stays as it was; nor are replays of calls captured into
+ * graphs: those must have finished, and such graphs must not run again).  The caller's regions are
+ * untouched.  NULL is accepted.
  * No passage: library infrastructure (the handle's lifetime). */
 KV_API int kv_pool_destroy(kv_pool *pool);
 
@@ -482,7 +483,7 @@ KV_API int kv_remap_tables(kv_pool *pool, const kv_page_copy *moves, int32_t n, 
  * elem_bytes a multiple of 16 (KV_ERR_ALIGN).  create allocates all device memory the plan
  * will use, on the current device, which is then the pool's, and waits for the device; it must
  * not be made while a stream captures (KV_ERR_HIP).  destroy waits for the device to be idle
- * first; NULL is accepted.  A plan is destroyed before its pool, and graphs that hold its calls do not
+ * first (KV_ERR_HIP, and the plan stays, while a stream captures, as for kv_pool_destroy); NULL is accepted.  A plan is destroyed before its pool, and graphs that hold its calls do not
  * run again.  No passage for this section: the attention that reads the cache the pages move. */
 KV_API int kv_attn_plan_create(kv_pool *pool, const kv_attn_desc *desc, kv_attn_plan **out);
 KV_API int kv_attn_plan_destroy(kv_attn_plan *plan);

@@ -346,6 +346,16 @@ int arena_commit(kv_pool *p, int64_t off, int64_t bytes, hipStream_t stream)
     return KV_OK;
 }
 
+int device_wait(int device)
+{
+    int dev = -1;
+    if (!HIP_OK(hipGetDevice(&dev))) return KV_ERR_HIP;
+    if (dev != device && !HIP_OK(hipSetDevice(device))) return KV_ERR_HIP;
+    const bool idle = HIP_OK(hipDeviceSynchronize());
+    if (dev != device) (void)hipSetDevice(dev);
+    return idle ? KV_OK : KV_ERR_HIP;
+}
+
 int device_setup(kv_pool *p)
 {
     int dev = -1;
@@ -382,19 +392,16 @@ using kvx::arena_commit;
 using kvx::arena_take;
 using kvx::device_setup;
 
-void device_teardown(kv_pool *p)
+// KV_ERR_HIP, and nothing freed, if the device cannot be waited for (a stream captures).
+int device_teardown(kv_pool *p)
 {
     // Every transfer's launch that reads the pool's device state (region table, error
     // word, span records) is fenced by its arena event, so waiting for the calls still in
     // flight is enough and other work on the device is left alone, unless the pool has
     // made calls with no event.
     if (p->unfenced) {
-        int dev = -1;
-        const bool other = hipGetDevice(&dev) == hipSuccess && dev != p->device;
-        if (other) (void)hipSetDevice(p->device);
-        (void)hipDeviceSynchronize();
-        if (other) (void)hipSetDevice(dev);
-        (void)hipGetLastError();
+        if (int rc = kvx::device_wait(p->device)) return rc;
+        p->unfenced = false;
     }
     if (p->device >= 0)
         for (int k = 0; k < p->arena.count; ++k)
@@ -402,6 +409,7 @@ void device_teardown(kv_pool *p)
     free_device_state(p);
     for (hipEvent_t &e : p->t_ev)
         if (e) (void)hipEventDestroy(e), e = nullptr;
+    return KV_OK;
 }
 
 int validate_tables(kv_pool *p, const kv_span *spans, int32_t n_spans, int direction,
@@ -808,7 +816,7 @@ int kv_pool_create(const kv_pool_desc *desc, kv_pool **out)
 int kv_pool_destroy(kv_pool *pool)
 {
     if (!pool) return KV_OK;
-    device_teardown(pool);
+    if (int rc = device_teardown(pool)) return rc;
     delete pool;
     return KV_OK;
 }

@@ -354,13 +354,8 @@ int kv_attn_plan_create(kv_pool *pool, const kv_attn_desc *desc, kv_attn_plan **
 int kv_attn_plan_destroy(kv_attn_plan *p)
 {
     if (!p) return KV_OK;
-    int dev = -1;
-    const bool other = hipGetDevice(&dev) == hipSuccess && dev != p->device;
-    if (other) (void)hipSetDevice(p->device);
-    (void)hipDeviceSynchronize();
-    (void)hipGetLastError();
+    if (int rc = kvx::device_wait(p->device)) return rc;  // its launches may still run
     plan_free(p);
-    if (other) (void)hipSetDevice(dev);
     return KV_OK;
 }
 

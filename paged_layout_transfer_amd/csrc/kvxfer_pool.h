@@ -70,6 +70,9 @@ bool hip_ok(hipError_t e, const char *where);
 // KV_ERR_ARG when another device is current now.
 int device_setup(kv_pool *p);
 
+// Waits until `device` is idle, whichever is current; KV_ERR_HIP where it cannot be waited for.
+int device_wait(int device);
+
 // Reserve a stretch of the pool's record arena for one call (the host waits for the
 // calls that still use it), and mark it as used by the work queued on `stream`.
 int arena_take(kv_pool *p, int64_t bytes, int64_t *off);

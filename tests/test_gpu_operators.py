@@ -3,6 +3,7 @@
 them together.  Every case is printed before its first launch."""
 from __future__ import annotations
 
+import ctypes
 import math
 
 import numpy as np
@@ -817,3 +818,35 @@ def test_an_error_right_after_the_last_one_was_read_is_not_lost():
             big.mul_(1.0)
             assert K.kv_pool_get_error(c.handle, side) == K.KV_DEVERR_BLOCK_RANGE
         assert K.kv_pool_get_error(c.handle, side) == 0
+
+
+@pytest.mark.parametrize("mode", [0, 2], ids=["global", "relaxed"])
+def test_nothing_is_freed_that_cannot_be_waited_for(mode):
+    """While a stream captures the device cannot be waited for: a plan, and a pool with copies in flight, then
+    stay as they are."""
+    region = torch.arange(64 * 4096, dtype=torch.int32, device="cuda").view(64, 4096)    # 16 KiB pages
+    regions = [region, region.clone()]
+    want = [r.clone() for r in regions]
+    pool = K.kv_pool_create(K.make_pool_desc(1, 2, 8, 64, 2, 16, 64, 16384, regions))
+    plan = K.kv_attn_plan_create(pool, K.make_attn_desc(8, K.KV_TYPE_BF16, K.KV_TYPE_BF16, 1, 1))
+    side, other, big = torch.cuda.Stream(), torch.cuda.Stream(), torch.ones(1 << 26, device="cuda")
+    graph = ctypes.c_void_p()
+    torch.cuda.synchronize()
+    say("destroy while a stream captures, mode", mode)
+    with torch.cuda.stream(other):
+        for _ in range(20):
+            big.mul_(1.0)
+        K.kv_copy_pages(pool, K.make_page_copies([(i, 32 + i, 16) for i in range(8)]), 0, 1, other)
+    begun = K._lib.hipStreamBeginCapture(ctypes.c_void_p(side.cuda_stream), mode)
+    codes = [K._lib.kv_attn_plan_destroy(ctypes.c_void_p(plan)), K._lib.kv_pool_destroy(ctypes.c_void_p(pool))]
+    K._lib.hipStreamEndCapture(ctypes.c_void_p(side.cuda_stream), ctypes.byref(graph))
+    K._lib.hipGetLastError()
+    torch.cuda.synchronize()
+    assert begun == 0 and codes == [K.KV_ERR_HIP, K.KV_ERR_HIP]
+    K.kv_copy_pages(pool, K.make_page_copies([(i, 40 + i, 16) for i in range(8)]), 0, 1, other)
+    torch.cuda.synchronize()
+    for r, w in zip(regions, want):
+        w[32:40], w[40:48] = w[:8], w[:8]
+        assert torch.equal(r, w)
+    K.kv_attn_plan_destroy(plan)
+    K.kv_pool_destroy(pool)
