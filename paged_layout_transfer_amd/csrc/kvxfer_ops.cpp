@@ -178,7 +178,7 @@ int kv_pool_block_refs(const kv_pool *p, int32_t id, int32_t *out)
 int kv_pool_fork_blocks(kv_pool *p, int64_t n_tokens, const int32_t *ids, int32_t *child_ids, kv_page_copy *tail)
 {
     if (!p || n_tokens < 0 || !tail || (n_tokens > 0 && (!ids || !child_ids))) return KV_ERR_ARG;
-    const int64_t bs = p->desc.block_size, pages = cdiv(n_tokens, bs), whole = n_tokens / bs;
+    const int64_t bs = p->desc.block_size, whole = n_tokens / bs, pages = whole + (n_tokens % bs != 0);
     if (pages > p->desc.num_blocks) return KV_ERR_RANGE;
     try {
         std::vector<int32_t> own(ids, ids + pages);

@@ -78,6 +78,17 @@ def test_fork_refuses_and_changes_nothing():
     K.kv_pool_destroy(p)
 
 
+@pytest.mark.parametrize("bs", [1, 16, 24])
+@pytest.mark.parametrize("tokens", [2**63 - 1, 2**63 - 16, 2**62, 65 * 24])
+def test_a_fork_of_more_tokens_than_the_pool_holds_is_out_of_range(bs, tokens):
+    p = _pool(bs=bs)
+    ids, child = np.zeros(64, np.int32), np.full(64, -1, np.int32)
+    tail = K.kv_page_copy()
+    rc = K._lib.kv_pool_fork_blocks(p, tokens, ids.ctypes.data, child.ctypes.data, ctypes.byref(tail))
+    assert rc == K.KV_ERR_RANGE and (child == -1).all()
+    K.kv_pool_destroy(p)
+
+
 @pytest.mark.parametrize("N,live,most", [(64, 20, 100), (64, 64, 8), (64, 0, 8), (200, 90, 7), (1000, 333, 1000), (1, 1, 1)])
 def test_compaction_pairs_highest_pages_with_lowest_holes(N, live, most):
     rng = np.random.default_rng(N + live)
