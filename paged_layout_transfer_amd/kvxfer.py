@@ -128,14 +128,19 @@ def _stream(s) -> int:
 
 # ---- entry points ------------------------------------------------------------------------
 
+_pages = {}  # (block_size, num_blocks) of the pools made here: how many ids a fork reads and writes
+
+
 def kv_pool_create(desc: kv_pool_desc) -> int:
     h = ctypes.c_void_p()
     _check(_lib.kv_pool_create(ctypes.byref(desc), ctypes.byref(h)), "kv_pool_create")
+    _pages[h.value] = desc.block_size, desc.num_blocks
     return h.value
 
 
 def kv_pool_destroy(pool: int) -> None:
     _check(_lib.kv_pool_destroy(pool), "kv_pool_destroy")
+    _pages.pop(pool, None)
 
 
 def kv_pool_alloc_blocks(pool: int, n: int) -> np.ndarray:
@@ -223,10 +228,14 @@ def kv_pool_block_refs(pool: int, block: int) -> int:
 
 
 def kv_pool_fork_blocks(pool: int, n_tokens: int, ids) -> tuple[np.ndarray, tuple[int, int, int] | None]:
-    """The child's block ids, and the (src, dst, n_tokens) copy that fills its last page or
-    None; ids holds the parent's blocks, one per page of n_tokens."""
-    ids = np.ascontiguousarray(ids, dtype=np.int32)
-    child, tail = ids.copy(), kv_page_copy()
+    """The child's block ids, one per page of n_tokens, and the (src, dst, n_tokens) copy that fills its last
+    page or None; ids holds the parent's blocks, those behind the last page unused."""
+    ids = np.ascontiguousarray(ids, dtype=np.int32).reshape(-1)
+    page, blocks = _pages[pool]
+    pages = -(-n_tokens // page)
+    if ids.size < pages <= blocks:      # more pages than the pool has: refused before an id is read
+        raise ValueError("%d block ids for %d pages" % (ids.size, pages))
+    child, tail = ids[:max(0, pages)].copy(), kv_page_copy()
     _check(_lib.kv_pool_fork_blocks(pool, n_tokens, ids.ctypes.data, child.ctypes.data, ctypes.byref(tail)),
            "kv_pool_fork_blocks")
     return child, (tail.src, tail.dst, tail.n_tokens) if tail.n_tokens else None

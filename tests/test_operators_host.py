@@ -89,6 +89,20 @@ def test_a_fork_of_more_tokens_than_the_pool_holds_is_out_of_range(bs, tokens):
     K.kv_pool_destroy(p)
 
 
+def test_a_fork_takes_as_many_ids_as_the_tokens_have_pages():
+    p = _pool()
+    ids = K.kv_pool_alloc_blocks(p, 5)
+    for few in ([], ids[:2]):
+        with pytest.raises(ValueError):
+            K.kv_pool_fork_blocks(p, 40, few)
+    child, tail = K.kv_pool_fork_blocks(p, 40, ids)     # the parent has room for more tokens
+    assert child.tolist() == [0, 1, 5] and tail == (2, 5, 8)
+    child, tail = K.kv_pool_fork_blocks(p, 0, ids)
+    assert child.size == 0 and tail is None
+    assert [K.kv_pool_block_refs(p, i) for i in range(6)] == [2, 2, 1, 1, 1, 1]
+    K.kv_pool_destroy(p)
+
+
 @pytest.mark.parametrize("N,live,most", [(64, 20, 100), (64, 64, 8), (64, 0, 8), (200, 90, 7), (1000, 333, 1000), (1, 1, 1)])
 def test_compaction_pairs_highest_pages_with_lowest_holes(N, live, most):
     rng = np.random.default_rng(N + live)
