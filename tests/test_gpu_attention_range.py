@@ -9,7 +9,7 @@ import torch
 
 import paged_reference as ref
 from paged_layout_transfer_amd import kvxfer as K
-from test_gpu_operators import Cache, deal, say, seqs_of
+from test_gpu_operators import Cache, attend_case, deal, say, seqs_of
 
 pytestmark = pytest.mark.gpu
 
@@ -183,3 +183,63 @@ def test_a_seen_infinity_counts_however_small_its_weight(lens, kind, held, dim, 
             assert inf.any() or held == "e4m3"
             fin = torch.isfinite(want)
             assert ((got - want).abs()[fin] <= tol[fin]).all()
+
+
+# a head to each wave of the few-rows kernel: heads a multiple of four, and work enough
+FORMS = {"few": (2, [(1, 700), (2, 300)]), "many": (2, [(50, 400), (70, 100), (130, 135)]),
+         "a_head_a_wave": (4, [(1 + i % 3, 240 + i) for i in range(260)])}
+
+
+@pytest.mark.parametrize("form", list(FORMS))
+@pytest.mark.parametrize("dim", [80, 128, 192, 256])
+@pytest.mark.parametrize("kind,held", [("bf16", "bf16"), ("f16", "e4m3")])
+def test_what_a_query_does_not_see_does_not_reach_it_at_other_widths(form, dim, kind, held):
+    """NaN, and infinities where the type has them, in unused pages, behind the last token, outside the
+    window, and in the newest token, which earlier queries of the call do not see."""
+    heads, lens = FORMS[form]
+    for window, poison in ((0, math.nan), (100, math.nan), (100, math.inf)):
+        if held == "e4m3" and poison == math.inf:
+            continue
+        with Cache(heads=heads, dim=dim, page=16, blocks=20 + sum(n // 16 + 1 for _, n in lens), kind=kind, cache=held) as c:
+            keep = torch.zeros(c.blocks, c.page, dtype=torch.bool)
+            for t, (q, n) in zip(deal(c, lens), lens):
+                j = torch.arange(max(0, n - q - window + 1) if window else 0, n)
+                keep[t.long()[j // 16], j % 16] = True
+                keep[int(t[(n - 1) // 16]), (n - 1) % 16] = False
+            bits = c.host.view(torch.uint8 if held == "e4m3" else torch.int16)
+            bits[:, ~keep] = torch.tensor([poison]).to(c.host.dtype).view(bits.dtype)
+            c.upload()
+            attend_case(c, lens, 2 * heads, window=window, label="poison %s" % poison)
+
+
+@pytest.mark.parametrize("form", list(FORMS))
+@pytest.mark.parametrize("dim", [80, 128, 192, 256])
+@pytest.mark.parametrize("kind,held", [("bf16", "bf16"), ("f16", "f16"), ("bf16", "e4m3")])
+@pytest.mark.parametrize("shape", [dict(), dict(window=40), dict(softcap=30.0, slopes=True), dict(window=40, softcap=200.0)], ids=str)
+def test_infinite_and_nan_values_at_other_widths(form, dim, kind, held, shape):
+    """Values of single cached tokens: the first one, one in the middle and the newest, an infinity of either
+    sign, both in one column, NaN, in the first and the last columns."""
+    heads, lens = FORMS[form]
+    with Cache(heads=heads, dim=dim, page=16, blocks=20 + sum(n // 16 + 1 for _, n in lens), kind=kind, cache=held) as c:
+        for t, (q, n) in zip(deal(c, lens), lens):
+            at = lambda j: c.host[1][int(t[j // 16]), j % 16]       # noqa: E731
+            at(n - 1)[1, 7], at(n // 3)[heads - 1, dim - 2] = math.nan, math.nan
+            if held != "e4m3":
+                at(0)[0, 3] = math.inf
+                at(n // 2)[0, 5] = -math.inf
+                at(n - 1)[0, 9], at(n - 2)[0, 9] = math.inf, -math.inf
+                at(n - 2)[heads - 1, dim - 1] = math.inf
+        c.upload()
+        attend_case(c, lens, 2 * heads, label="infinite values", **shape)
+
+
+@pytest.mark.parametrize("kind,held", [("bf16", "bf16"), ("f16", "f16"), ("bf16", "e4m3"), ("f16", "e4m3")])
+@pytest.mark.parametrize("dim", [136, 192, 240, 96, 48])
+@pytest.mark.parametrize("head_major", [False, True])
+def test_widths_between_those_of_the_kernels(kind, held, dim, head_major):
+    if held == "e4m3" and dim % 16:
+        dim += 8
+    lens = [(1, 700), (2, 33), (70, 70), (1, 300), (40, 500), (130, 131), (3, 3)]
+    with Cache(heads=2, dim=dim, page=24, blocks=200, head_major=head_major, kind=kind, cache=held, pad=32) as c:
+        attend_case(c, lens, 8)
+        attend_case(c, lens, 4, window=60, softcap=100.0, slopes=True)
