@@ -192,7 +192,7 @@ int kv_pool_fork_blocks(kv_pool *p, int64_t n_tokens, const int32_t *ids, int32_
     if (pages > whole && p->blocks.n_free < 1) return KV_ERR_OOM;
     if (int rc = p->blocks.share((int32_t)whole, ids)) return rc;
     const int32_t last = pages > whole ? ids[whole] : -1;  // child_ids may be ids
-    std::memmove(child_ids, ids, (size_t)whole * sizeof(int32_t));
+    if (whole > 0) std::memmove(child_ids, ids, (size_t)whole * sizeof(int32_t));
     *tail = kv_page_copy{0, 0, 0};
     if (pages > whole) {
         int32_t fresh = -1;
