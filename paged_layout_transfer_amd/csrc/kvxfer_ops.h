@@ -68,7 +68,7 @@ int launch_remap(const RemapLaunch &a, hipStream_t stream);
 // Rows of a piece of the many-rows kernel: 32 to a wave; at the widest heads a wave's
 // registers leave room for four waves only.
 KVX_HD int32_t rows_many(int dim) { return dim > 128 ? 128 : 256; }
-// With fewer rows, every second wave only helps loading (chosen by build_plan).
+// With fewer rows, waves 4 to 7 only help loading (chosen by build_plan).
 #define KVX_ROWS_HALF 128
 
 // One workgroup's piece of attention: rows [row0, row0 + rows) of one

@@ -142,9 +142,11 @@ __device__ __forceinline__ float e4m3_of(float x, float scale)
 
 // Four workgroups to an item, two of its tokens each.  A thread owns eight values of a token's row
 // (of its keys, then its values): block ids and rows of both tokens first, then the stores.  Bound by
-// the latency of that chain: 3.5 us for 64 tokens of a decode step; a pass with its launch 13.5 us for
-// 7874 tokens in chunks into an 8-bit pool (48 MB; one workgroup to an item, four tokens at a time, 15.0,
-// eight 15.8), 11.5 for 4000 tokens of 8 x 256 bf16 (66 MB; 12.5).
+// the latency of that chain: 3.5 us for 64 tokens of a decode step, 12.1 us a pass with its launch for 7874 tokens in
+// chunks into a 16-bit pool (64 MB), 11.5 for 4000 tokens of 8 x 256 bf16 (66 MB).  An 8-bit pool
+// moves 48 MB of the same chunks in 13.5 to 15.0 us: the correctly rounded quotient of each element costs 4 us of
+// them (with a product in its place 11.2).  One workgroup to an item, four tokens at a time, took 15.0 where this
+// took 13.5, eight at a time 15.8.
 template <class T, bool E4M3>
 __global__ __launch_bounds__(kThreads) void append_tokens(const AttnLaunch a)
 {

@@ -1,6 +1,8 @@
 // kvxfer_plan.h -- host planning of one step's attention: which pieces of work there are
-// and how they are split over the keys (host only; no HIP call, no allocation once the
-// vectors have their capacity).
+// and how they are split over the keys (host only; no HIP call; the vectors keep their
+// capacity, and std::stable_sort takes a buffer for the call).  On a host of the measured card a set takes 6 us for one
+// short decode, 9 for one on 32 K tokens, 17 for 16 sequences, 26 for 64 or for eight ragged turns, 53 for 256,
+// its upload's call included.
 #pragma once
 #include <algorithm>
 #include <functional>
@@ -101,8 +103,10 @@ inline int64_t parts_at(const std::vector<AttnItem> &whole, int64_t share, int32
 struct SplitCost {
     int64_t whole, cut, join, min_tiles;
 };
+// Measured in tiles of 128-wide 16-bit heads without a cap, and used for all: a 64-wide tile costs less, a capped
+// one more, and with them the costs in tiles.
 constexpr SplitCost kCostFew{2, 2, 10, 2}, kCostMany{1, 4, 4, 8}, kCostHalf{1, 4, 5, 8};
-// A tile with half of the waves at work takes 72 hundredths of the time of one with all (1.5 and
+// A tile with waves 0 to 3 at work takes 72 hundredths of the time of one with all (1.5 and
 // 2.1 us, 128-wide heads; 512 new tokens on 16 K cached, cut to one round either way: 217 and 155 us).
 constexpr int64_t kHalfTile = 72;
 
