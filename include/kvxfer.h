@@ -157,6 +157,8 @@ extern "C" {
 #define KV_TYPE_F16 0  /* IEEE half */
 #define KV_TYPE_BF16 1 /* bfloat16 */
 #define KV_TYPE_E4M3 2 /* 8-bit float, OCP e4m3fn (pools only) */
+#define KV_TYPE_MX4 3  /* 4-bit floats with a shared power of two for each 32 (pools only): see
+                          "Rows of KV_TYPE_MX4" below */
 
 /* kv_attn_desc.flags */
 #define KV_ATTN_FULL 0x1 /* every query sees every cached token (no causal mask) */
@@ -170,7 +172,13 @@ extern "C" {
 #define KV_MAX_PAGE_COPIES 65536 /* records of one kv_copy_pages or kv_remap_tables call */
 #define KV_MAX_SEQS 4096         /* sequences of one attention plan */
 #define KV_MAX_ATTN_DIM 256      /* head_dim of the attention operators */
+#define KV_MAX_SHIFTS 4096       /* records of one kv_rotate_cached call */
 
+/* kv_rotation_desc.pairing: which two elements of a head turn together, of n pairs */
+#define KV_ROT_HALVES 0   /* i and i + n */
+#define KV_ROT_ADJACENT 1 /* 2i and 2i + 1 */
+
+typedef struct kv_rotation kv_rotation; /* opaque, owned by the library */
 typedef struct kv_pool kv_pool; /* opaque, owned by the library */
 typedef struct kv_ring kv_ring; /* opaque, owned by the library */
 typedef struct kv_attn_plan kv_attn_plan; /* opaque, owned by the library */
@@ -254,7 +262,7 @@ typedef struct {
     int32_t num_q_heads; /* query heads, a multiple of the pool's num_heads: query head h reads
                             the cache's head h / (num_q_heads / num_heads) */
     int32_t q_type;      /* of q, out and the appended k and v: KV_TYPE_F16 or KV_TYPE_BF16 */
-    int32_t kv_type;     /* of the pool: q_type, or KV_TYPE_E4M3 */
+    int32_t kv_type;     /* of the pool: q_type, KV_TYPE_E4M3 or KV_TYPE_MX4 */
     int32_t window;      /* > 0: a query sees its own token and the window - 1 before it; 0: all
                             before it.  KV_ERR_ARG together with KV_ATTN_FULL */
     int32_t flags;       /* KV_ATTN_* */
@@ -286,6 +294,39 @@ typedef struct {
                                                0: off */
     float k_scale, v_scale;                 /* as in kv_append_args */
 } kv_attend_args;
+
+typedef struct {
+    int32_t pairs;          /* n, a multiple of 4 up to KV_MAX_ATTN_DIM / 2: the first 2n elements of a head turn */
+    int32_t pairing;        /* KV_ROT_HALVES or KV_ROT_ADJACENT */
+    float amplitude;        /* of the turned elements, finite, > 0; 1 for a plain rotation */
+    const double *inv_freq; /* host array of n angles a position turns pair i by, in radians, 0 .. 2^20 */
+} kv_rotation_desc;
+
+/* Strides as in kv_attend_args. */
+typedef struct {
+    const void *q;                          /* device, [n_tokens][num_q_heads][head_dim], q_type; NULL: k only */
+    void *q_out;                            /* device, the same shape and type; may be q with its strides */
+    const int32_t *positions;               /* device, [n_tokens]; NULL: each token's place in the cache */
+    int64_t q_token_stride, q_head_stride;
+    int64_t out_token_stride, out_head_stride;
+} kv_rotate_args;
+
+/* Cached tokens [t_begin, t_end) of one sequence, whose keys turn by `delta` positions. */
+typedef struct {
+    const int32_t *block_table; /* device array */
+    int64_t table_len;          /* entries in block_table; >= ceil(t_end / block_size), < 2^31 */
+    int64_t t_begin, t_end;     /* 0 <= t_begin <= t_end <= 2^31 - 4097; empty: nothing */
+    int32_t delta;              /* positions, either sign */
+} kv_shift;
+
+/* Strides as in kv_attend_args; a layer stride is only used with more than one layer. */
+typedef struct {
+    void *k, *v;                            /* device, [layers][n_tokens][num_heads][head_dim], q_type; NULL: not read */
+    int64_t k_layer_stride, k_token_stride, k_head_stride;
+    int64_t v_layer_stride, v_token_stride, v_head_stride;
+    int64_t n_tokens;                       /* rows the arrays hold */
+    float k_scale, v_scale;                 /* as in kv_append_args */
+} kv_read_args;
 
 /* ---- pool ------------------------------------------------------------------ */
 
@@ -476,11 +517,27 @@ KV_API int kv_remap_tables(kv_pool *pool, const kv_page_copy *moves, int32_t n, 
 
 /* ---- new tokens: append and attention -------------------------------------------- */
 
+/* Rows of KV_TYPE_MX4.  A pool of 4-bit values is described to kv_pool_create by its bytes: elem_bytes 1 and
+ * head_dim the bytes R of one head's row, a multiple of 4.  The row holds G = R / 17 (rounded down) groups of 32
+ * elements, so the operators' head_dim is 32 G (at most KV_MAX_ATTN_DIM): 16 G bytes of elements, then
+ * G bytes of scales, then what is left of R, which nothing reads or writes.  Element 2b is the low
+ * half of byte b, 2b + 1 the high half: a sign bit over three bits of {0, 0.5, 1, 1.5, 2, 3, 4, 6} (OCP e2m1).  Scale
+ * byte e stands for 2^(e - 127), 255 for NaN (OCP e8m0); an element is its value times its group's scale.  Transfers,
+ * page copies, forks and compaction move such pools like any other.
+ * What is written: the scale is the smallest power of two 2^s, s >= -126, with |x| <= 7 * 2^s for all
+ * 32 values, and each element is x / 2^s rounded to nearest even and saturated at 6: values over 6 are off by
+ * no more than others of their size, and the group keeps the finer scale.  A group that holds an infinity or NaN becomes NaN
+ * whole (scale byte 255, elements 0).  What is read is rounded to q_type (exact but for halves below 2^-24, and past the type's range).
+ * kv_mx4_row_bytes: the smallest R for head_dim elements with which a token of num_heads rows is the multiple
+ * of 16 bytes that a pool needs.  head_dim a multiple of 32 up to KV_MAX_ATTN_DIM (KV_ERR_ARG).
+ * Host only.  No passage. */
+KV_API int kv_mx4_row_bytes(int32_t head_dim, int32_t num_heads, int32_t *out);
+
 /* A plan holds, on the device, one step's sequences, the split of their attention over the
  * chip, and the workspace of partial results (up to 200 MiB); it is set once a step and used
- * by every layer.  The pool has num_kv 2, elem_bytes 1 for KV_TYPE_E4M3 and 2 else, head_dim <=
+ * by every layer.  The pool has num_kv 2, elem_bytes 1 for KV_TYPE_E4M3 and KV_TYPE_MX4 and 2 else, head_dim <=
  * KV_MAX_ATTN_DIM, and num_q_heads * max_tokens < 2^31 (else KV_ERR_ARG), and head_dim *
- * elem_bytes a multiple of 16 (KV_ERR_ALIGN).  create allocates all device memory the plan
+ * elem_bytes a multiple of 16, of 4 for KV_TYPE_MX4 (KV_ERR_ALIGN).  create allocates all device memory the plan
  * will use, on the current device, which is then the pool's, and waits for the device; it must
  * not be made while a stream captures (KV_ERR_HIP).  destroy waits for the device to be idle
  * first (KV_ERR_HIP, and the plan stays, while a stream captures, as for kv_pool_destroy); NULL is accepted.  A plan is destroyed before its pool, and graphs that hold its calls do not
@@ -502,8 +559,8 @@ KV_API int kv_attn_plan_set(kv_attn_plan *plan, const kv_seq *seqs, int32_t n, h
 
 /* Writes the new tokens' k and v rows into their pages of one layer: the token at position p
  * goes to slot p % block_size of block block_table[p / block_size].  An e4m3 pool gets
- * x / scale, rounded to nearest even and saturated at +-448; NaN stays NaN.  Nothing else is
- * written, and rows of no sequence are not read.  Two sequences must not write one pool token.  A block id
+ * x / scale, rounded to nearest even and saturated at +-448; NaN stays NaN; a KV_TYPE_MX4 pool gets rows as
+ * above.  Nothing else is written, and rows of no sequence are not read.  Two sequences must not write one pool token.  A block id
  * out of range is skipped and reported (kv_pool_get_error).  Errors: KV_ERR_ARG (layer, null or
  * negative arguments, scales, a sequence with q_len > kv_len, another device current),
  * KV_ERR_ALIGN, KV_ERR_RANGE (n_tokens below a row the plan names, an array past its allocation).
@@ -534,6 +591,50 @@ KV_API int kv_append_tokens(kv_attn_plan *plan, int32_t layer, const kv_append_a
  * rows of out that overlap.
  * Captured, a call holds the kernels for any sequences within the plan's limits. */
 KV_API int kv_attend(kv_attn_plan *plan, int32_t layer, const kv_attend_args *args, hipStream_t stream);
+
+/* Position rotation.  A token at position p turns pair i of a head by p * inv_freq[i]: of the pair's elements
+ * (x, y) it makes amplitude * (x cos - y sin, x sin + y cos); elements from 2 * pairs on stay as they are.  Angles
+ * are taken as fractions of a turn in 64 bits, p times inv_freq[i] / 2 pi rounded to 2^-64, so that they are
+ * good to |p| 2^-64 turns at any position.  Products and sums are held in 32 bits, in 64 for keys on their
+ * way into a KV_TYPE_MX4 pool, and rounded once to what is written.
+ * create copies the frequencies to the current device, where the rotation is then used, and waits for the
+ * copy (KV_ERR_HIP while a stream captures); KV_ERR_ARG for pairs not 1 .. KV_MAX_ATTN_DIM / 2, an unknown
+ * pairing, or frequencies or an amplitude out of range, KV_ERR_ALIGN for pairs no multiple of 4.  destroy waits for the device
+ * like kv_attn_plan_destroy; NULL is accepted.  No passage. */
+KV_API int kv_rotation_create(const kv_rotation_desc *desc, kv_rotation **out);
+KV_API int kv_rotation_destroy(kv_rotation *rotation);
+
+/* kv_append_tokens with the rotation applied on the way, one launch: the new tokens' k rows are rotated, each to its
+ * position, and written to their pages with the v rows; their q rows are rotated into q_out.  Rotated
+ * values are rounded once, to the pool's type (after the division by k_scale) or q_type.  positions[row] is a
+ * token's position, of either sign; NULL takes its place in the cache.  Rows of no sequence are neither read
+ * nor written.  q_out may be q with its strides; otherwise it overlaps nothing that the call reads.
+ * Errors and capture as kv_append_tokens; also KV_ERR_ARG for a rotation wider than head_dim or of another
+ * device, and rows of q_out that overlap.  A bad block id skips the token's k and v, not its q. */
+KV_API int kv_append_rotated(kv_attn_plan *plan, int32_t layer, const kv_rotation *rotation, const kv_rotate_args *rotate,
+                             const kv_append_args *args, hipStream_t stream);
+
+/* The inverse of append: the new tokens' places in the cache of layers [layer_begin, layer_end), read as
+ * q_type rows: 16-bit pools' rows as they are, k_scale or v_scale times an e4m3 element, KV_TYPE_MX4 rows' values, each
+ * rounded once.  A plan whose sequences have q_len = kv_len reads caches whole.  Rows of no sequence, and of tokens
+ * whose block id is out of range (reported), are left as they were.  One launch.  Errors and capture as
+ * kv_append_tokens; also KV_ERR_ARG for an empty layer range, no array at all, and rows of an array that overlap. */
+KV_API int kv_read_tokens(kv_attn_plan *plan, int32_t layer_begin, int32_t layer_end, const kv_read_args *args,
+                          hipStream_t stream);
+
+/* Moves cached keys to other positions: in layers [layer_begin, layer_end) the keys of each record's tokens turn
+ * by delta positions, in place, without amplitude, and are rounded to the pool's type again; values stay.  For
+ * tokens that were appended rotated and whose places change: the middle of a conversation is dropped and the rest
+ * moves up, or a reloaded chunk is used behind another prefix.  kv_type is the pool's element type, the pool as
+ * for kv_attn_plan_create.  An e4m3 element saturates at +-448; its scale does not matter.  No page position may
+ * be named twice, and pages that others share turn for them too (kv_pool_fork_blocks, kv_copy_pages).  A block
+ * id out of range is skipped and reported.  shifts is a host array of n (0 .. KV_MAX_SHIFTS) records, the tables are read
+ * when the call runs.  One launch.  Errors: KV_ERR_ARG, KV_ERR_ALIGN, KV_ERR_RANGE as for kv_attn_plan_create and
+ * kv_attn_plan_set, KV_ERR_ARG for a rotation wider than head_dim or of another device.  Under capture a call of
+ * at most 64 records that are not empty is captured as its kernel once the pool has made a call outside the
+ * capture; any other is refused with KV_ERR_CAPTURE. */
+KV_API int kv_rotate_cached(kv_pool *pool, const kv_rotation *rotation, int32_t kv_type, const kv_shift *shifts, int32_t n,
+                            int32_t layer_begin, int32_t layer_end, hipStream_t stream);
 
 /* Synchronizes `stream`, then reads and clears the pool's sticky device error
  * word.  *out_bits receives KV_DEVERR_* bits (0 if none); the return value is
@@ -595,7 +696,7 @@ KV_API const char *kv_strerror(int code);
 
 /* Library version: major*10000 + minor*100 + patch (KV_VERSION of the header the
  * library was built with).  No passage: library infrastructure. */
-#define KV_VERSION 300
+#define KV_VERSION 400
 KV_API int kv_version(void);
 
 /* The hipError_t of the last HIP runtime call that failed inside the library on

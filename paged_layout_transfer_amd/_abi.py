@@ -41,8 +41,12 @@ KV_MAX_ATTN_DIM = 256
 KV_TYPE_F16 = 0
 KV_TYPE_BF16 = 1
 KV_TYPE_E4M3 = 2
+KV_TYPE_MX4 = 3
+KV_MAX_SHIFTS = 4096
+KV_ROT_HALVES = 0
+KV_ROT_ADJACENT = 1
 KV_ATTN_FULL = 0x1
-KV_VERSION = 300
+KV_VERSION = 400
 
 
 class kv_pool_desc(ctypes.Structure):
@@ -103,6 +107,29 @@ class kv_attend_args(ctypes.Structure):
                 ("out_token_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
                 ("n_tokens", ctypes.c_int64), ("scale", ctypes.c_float), ("softcap", ctypes.c_float),
                 ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
+class kv_rotation_desc(ctypes.Structure):
+    _fields_ = [("pairs", ctypes.c_int32), ("pairing", ctypes.c_int32), ("amplitude", ctypes.c_float),
+                ("inv_freq", ctypes.POINTER(ctypes.c_double))]
+
+
+class kv_rotate_args(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("q_out", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("out_token_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64)]
+
+
+class kv_shift(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("table_len", ctypes.c_int64),
+                ("t_begin", ctypes.c_int64), ("t_end", ctypes.c_int64), ("delta", ctypes.c_int32)]
+
+
+class kv_read_args(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_layer_stride", ctypes.c_int64), ("k_token_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+                ("v_layer_stride", ctypes.c_int64), ("v_token_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+                ("n_tokens", ctypes.c_int64), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
 
 
 def _addr(x) -> int:
@@ -193,6 +220,51 @@ def make_attend_args(q, out, lse=None, *, n_tokens: int, scale: float, softcap: 
     strides; lse: [n_tokens][query heads] float32 or None."""
     return kv_attend_args(_addr(q), _addr(out), _addr(lse), _addr(alibi_slopes), *_strides(q, q_strides),
                           *_strides(out, out_strides), n_tokens, scale, softcap, k_scale, v_scale)
+
+
+def make_rotation_desc(inv_freq, pairing: int = KV_ROT_HALVES, amplitude: float = 1.0) -> kv_rotation_desc:
+    """inv_freq: the angle in radians by which one position turns each pair."""
+    freq = [float(f) for f in inv_freq]
+    arr = (ctypes.c_double * max(1, len(freq)))(*freq)
+    d = kv_rotation_desc(len(freq), pairing, amplitude, ctypes.cast(arr, ctypes.POINTER(ctypes.c_double)))
+    d._freq_keepalive = arr
+    return d
+
+
+def make_rotate_args(q=None, q_out=None, positions=None, q_strides=None, out_strides=None) -> kv_rotate_args:
+    """q and q_out: [n_tokens][query heads][dim] tensors, or device addresses with their (token, head) strides, or
+    None; positions: [n_tokens] int32 or None (the tokens' places in the cache)."""
+    none = (0, 0)
+    return kv_rotate_args(_addr(q), _addr(q_out), _addr(positions), *(none if q is None else _strides(q, q_strides)),
+                          *(none if q_out is None else _strides(q_out, out_strides)))
+
+
+def make_shifts(shifts: Iterable) -> ctypes.Array:
+    """shifts: (block_table, table_len, t_begin, t_end, delta) tuples; block_table is a device address or tensor."""
+    shifts = list(shifts)
+    arr = (kv_shift * max(1, len(shifts)))()
+    for i, (tbl, n, t0, t1, delta) in enumerate(shifts):
+        arr[i] = kv_shift(_addr(tbl), int(n), int(t0), int(t1), int(delta))
+    arr._n = len(shifts)
+    return arr
+
+
+def _layer_strides(x, strides):
+    if x is None:
+        return 0, 0, 0
+    if strides is not None:
+        return tuple(int(s) for s in strides)
+    if x.dim() == 3:
+        return (0, *_strides(x, None))
+    return (x.stride(0), *_strides(x[0], None))
+
+
+def make_read_args(k=None, v=None, *, n_tokens: int, k_scale: float = 1.0, v_scale: float = 1.0, k_strides=None,
+                   v_strides=None) -> kv_read_args:
+    """k and v: [layers][n_tokens][heads][dim] tensors ([n_tokens][heads][dim] for one layer), or device addresses
+    with their (layer, token, head) strides, or None."""
+    return kv_read_args(_addr(k), _addr(v), *_layer_strides(k, k_strides), *_layer_strides(v, v_strides), n_tokens,
+                        k_scale, v_scale)
 
 
 def _nspans(spans) -> int:

@@ -12,7 +12,8 @@ LIB = os.path.join(HERE, "libkvxfer.so")
 # the transfer path, then the operators on the cache beside it
 SOURCES = [os.path.join(CSRC, "kvxfer.cpp"), os.path.join(CSRC, "kvxfer_kernels.hip")]
 OPERATORS = [os.path.join(CSRC, f) for f in ("kvxfer_ops.cpp", "kvxfer_pages.hip", "kvxfer_attn_f16.hip",
-                                             "kvxfer_attn_bf16.hip")]
+                                             "kvxfer_attn_bf16.hip", "kvxfer_attn_mx4_f16.hip",
+                                             "kvxfer_attn_mx4_bf16.hip", "kvxfer_rotate.cpp", "kvxfer_rotate.hip")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
@@ -42,7 +43,7 @@ def build_library(force: bool = True) -> str:
              "-c", src, "-o", obj])
         return obj
 
-    with ThreadPoolExecutor(max_workers=4) as pool:
+    with ThreadPoolExecutor(max_workers=8) as pool:
         objs = list(pool.map(compile_one, SOURCES + OPERATORS))
     tmp = LIB + ".tmp"
     run([HIPCC, "--offload-arch=gfx950", "-fPIC", "-shared", *objs, "-o", tmp])

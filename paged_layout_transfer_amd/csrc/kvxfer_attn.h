@@ -1,5 +1,6 @@
 // kvxfer_attn.h -- attention of new tokens over a paged cache: device code, instantiated
-// for one query type by kvxfer_attn_f16.hip and kvxfer_attn_bf16.hip.
+// for one query type by kvxfer_attn_f16.hip and kvxfer_attn_bf16.hip, over mx4 pools by
+// kvxfer_attn_mx4_f16.hip and kvxfer_attn_mx4_bf16.hip.
 //
 // Mathematics.  For a query row and keys taken tile by tile, with x_j the score in base 2
 // (score * log2 e) and m the running maximum, the kernel keeps l = sum 2^(x_j - m) and
@@ -20,40 +21,9 @@
 
 #include <type_traits>
 
-#include "kvxfer_ops.h"
+#include "kvxfer_device.h"
 
 namespace kvx {
-
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef short i16x4 __attribute__((ext_vector_type(4)));
-#define KVX_GLOBAL __attribute__((address_space(1)))
-#define KVX_LDS __attribute__((address_space(3)))
-#define KVX_CONST __attribute__((address_space(4)))
-
-// A plan record, the same for the whole workgroup and not written while kernels run: read
-// through the constant space, by scalar loads into scalar registers.
-template <class Rec>
-__device__ __forceinline__ Rec plan_record(const Rec *at)
-{
-    constexpr int kWords = sizeof(Rec) / 4;
-    union {
-        Rec rec;
-        uint32_t word[kWords];
-    } u;
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) u.word[i] = ((const KVX_CONST uint32_t *)at)[i];
-    return u.rec;
-}
-
-template <class T>
-struct Vec {
-    typedef T x2 __attribute__((ext_vector_type(2)));
-    typedef T x4 __attribute__((ext_vector_type(4)));
-    typedef T x8 __attribute__((ext_vector_type(8)));
-};
 
 __device__ __forceinline__ f32x4 mfma16(Vec<_Float16>::x8 a, Vec<_Float16>::x8 b, f32x4 c)
 {
@@ -70,22 +40,6 @@ __device__ __forceinline__ f32x16 mfma32(Vec<_Float16>::x8 a, Vec<_Float16>::x8 
 __device__ __forceinline__ f32x16 mfma32(Vec<__bf16>::x8 a, Vec<__bf16>::x8 b, f32x16 c)
 {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
-}
-
-// Four e4m3 values (one word) as T: every one is a value of both 16-bit types.
-template <class T>
-__device__ __forceinline__ typename Vec<T>::x4 from_e4m3(uint32_t w)
-{
-    typedef typename Vec<T>::x2 T2;
-    T2 a, b;
-    if constexpr (__is_same(T, __bf16)) {
-        a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.f, false);
-        b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.f, true);
-    } else {
-        a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.f, false);
-        b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.f, true);
-    }
-    return typename Vec<T>::x4{a[0], a[1], b[0], b[1]};
 }
 
 // Whether a 16-bit value is an infinity or NaN.
@@ -164,6 +118,36 @@ struct Lost {
         return x != x;
     }
 };
+
+// How pool rows are read: the values of one load of the few-rows kernel (a lane in four shares a row, so an mx4 load is
+// at most a quarter of it: 32 values, or 16 of a 64-wide row), their bytes, and eight of them as T.
+template <int CACHE, int DP>
+constexpr int cache_values() { return CACHE == kHalves ? 8 : CACHE == kE4m3 ? 16 : DP == 64 ? 16 : 32; }
+template <int CACHE>
+constexpr int cache_bytes(int values) { return CACHE == kHalves ? 2 * values : CACHE == kE4m3 ? values : values / 2; }
+template <int BYTES>
+struct Words;
+template <>
+struct Words<4> {
+    typedef uint32_t type;
+};
+// mx4 rows start at multiples of four bytes
+template <>
+struct Words<8> {
+    typedef u32x2 type __attribute__((aligned(4)));
+};
+template <>
+struct Words<16> {
+    typedef u32x4 type __attribute__((aligned(4)));
+};
+template <class T, int CACHE, class R>
+__device__ __forceinline__ typename Vec<T>::x8 widen8(const R &r, int u)
+{
+    if constexpr (CACHE == kE4m3)
+        return __builtin_shufflevector(from_e4m3<T>(r[2 * u]), from_e4m3<T>(r[2 * u + 1]), 0, 1, 2, 3, 4, 5, 6, 7);
+    else
+        return __builtin_bit_cast(typename Vec<T>::x8, r);
+}
 
 // Rows of a tile in shared memory, in values.  Key rows are one 16-byte chunk longer than
 // their values, so that the 16 lanes that read one chunk of 16 rows meet all banks; value rows 64
@@ -385,15 +369,17 @@ __device__ __forceinline__ void store_lse(const AttnLaunch &a, int64_t row, int3
 // bf16 heads, 4 query heads to a cache head: 32 sequences of 1 K to 64 K tokens 306 us, 5.7 TB/s;
 // one of 32 K 28 us and 6 us to join; a context that one step of each wave covers 7 us, the latency of
 // record, block id, rows and the way out.
-template <class T, bool E4M3, int DP, int SHAPED>
+template <class T, int CACHE, int DP, int SHAPED>
 __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_few(const AttnLaunch a)
 {
     typedef typename Vec<T>::x8 T8;
     typedef typename Vec<T>::x4 T4;
     constexpr int kStep = 32;                         // keys of one wave's step
     constexpr int kS = DP / 32;                       // contraction steps of the first product
-    constexpr int kLoads = E4M3 ? DP / 64 : DP / 32;  // 16-byte loads of a lane for one key row
-    constexpr int kVals = E4M3 ? 16 : 8;              // values of one load
+    constexpr int kVals = cache_values<CACHE, DP>();  // values of a lane's load: 16 bytes, or 8
+    constexpr int kLoads = DP / (4 * kVals);          // loads of a lane for one key row
+    constexpr int kBytes = cache_bytes<CACHE>(kVals);
+    typedef typename Words<kBytes>::type Load;
     constexpr int kRow = value_row<DP>();
     // each wave's values, then its 16 rows of 32-bit results
     constexpr int kSlice = kStep * kRow * 2 > 16 * DP * 4 ? kStep * kRow * 2 : 16 * DP * 4;
@@ -416,9 +402,8 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_few(const AttnL
     const int n = lane & 15, g = lane >> 4;
     T *tile = (T *)(shared + wave * kSlice);
 
-    // The lane's row, and its query as the first product's right operand.  Lane group g
-    // holds, for contraction step c, columns 32 c + 8 g (16-bit pools) or, so that one
-    // 16-byte load of an 8-bit key row serves two steps, 64 (c / 2) + 16 g + 8 (c mod 2).
+    // The lane's row, and its query as the first product's right operand.  One load of a key row
+    // serves kVals / 8 contraction steps: lane group g holds, for step u of load c, columns (4 c + g) kVals + 8 u.
     const uint32_t R = (uint32_t)(s.row0 + (n < s.rows ? n : s.rows - 1));
     const int32_t tok = (int32_t)div_by(R, a.group_magic, a.group_shift);
     const int32_t pos = s.first + tok;
@@ -426,45 +411,51 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_few(const AttnL
     float slope = 0.f;
     if (SHAPED && a.slopes) slope = a.slopes[s.head * a.group + (int32_t)R - tok * a.group] * 1.4426950408889634f;
 
-    u32x4 kr[2][kLoads], vr[2][kLoads];
+    struct Rows {
+        Load r[2][kLoads];
+        uint32_t e[2][CACHE == kMx4 ? kLoads : 1];  // mx4: the scale bytes
+    };
+    Rows kr, vr;
     const int32_t i1 = s.tile1 * 2;
     int32_t i = s.tile0 * 2 + first;
     auto start = [&](int32_t i) { return s.walk.start(i >> 1) + (i & 1) * kStep; };
     auto key = [&](int32_t i, int t) { return seen_key(s, start(i) + 16 * t + n); };
     const bool whole_rows = a.dim == DP;
-    auto load = [&](u32x4(&r)[2][kLoads], const uint8_t *base, const int64_t(&off)[2]) __attribute__((always_inline)) {
+    auto load = [&](Rows &to, const uint8_t *base, const int64_t(&off)[2]) __attribute__((always_inline)) {
+        auto one = [&](int t, int c) __attribute__((always_inline)) {
+            to.r[t][c] = *(const KVX_GLOBAL Load *)(base + off[t] + (4 * c + g) * kBytes);
+            if constexpr (CACHE == kMx4)
+                to.e[t][c] = *(const KVX_GLOBAL uint8_t *)(base + off[t] + (a.dim / 2 + (4 * c + g) * kVals / KVX_MX4_GROUP));
+        };
         if (whole_rows) {
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int c = 0; c < kLoads; ++c)
-                    r[t][c] = *(const KVX_GLOBAL u32x4 *)(base + off[t] + c * 64 + g * 16);
+                for (int c = 0; c < kLoads; ++c) one(t, c);
         } else {
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int c = 0; c < kLoads; ++c) {
-                    r[t][c] = u32x4{0, 0, 0, 0};
-                    if (c * 4 * kVals + g * kVals < a.dim)
-                        r[t][c] = *(const KVX_GLOBAL u32x4 *)(base + off[t] + c * 64 + g * 16);
+                    to.r[t][c] = Load{};
+                    if constexpr (CACHE == kMx4) to.e[t][c] = 0;
+                    if ((4 * c + g) * kVals < a.dim) one(t, c);
                 }
         }
+    };
+    // values 8 u .. 8 u + 7 of a load
+    auto widen = [&](const Rows &from, int t, int c, int u) __attribute__((always_inline)) {
+        if constexpr (CACHE == kMx4) return from_mx4<T>(from.r[t][c][u], mx4_scale(from.e[t][c]));
+        else return widen8<T, CACHE>(from.r[t][c], u);
     };
     auto put_values = [&]() __attribute__((always_inline)) {  // to shared memory, row-major
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int c = 0; c < kLoads; ++c) {
-                T *to = tile + (16 * t + n) * kRow + c * 4 * kVals + g * kVals;
-                if constexpr (E4M3) {
-                    const T4 w0 = from_e4m3<T>(vr[t][c][0]), w1 = from_e4m3<T>(vr[t][c][1]);
-                    const T4 w2 = from_e4m3<T>(vr[t][c][2]), w3 = from_e4m3<T>(vr[t][c][3]);
-                    *(T8 *)to = __builtin_shufflevector(w0, w1, 0, 1, 2, 3, 4, 5, 6, 7);
-                    *(T8 *)(to + 8) = __builtin_shufflevector(w2, w3, 0, 1, 2, 3, 4, 5, 6, 7);
-                } else {
-                    *(u32x4 *)to = vr[t][c];
-                }
-            }
+            for (int c = 0; c < kLoads; ++c)
+#pragma unroll
+                for (int u = 0; u < kVals / 8; ++u)
+                    *(T8 *)(tile + (16 * t + n) * kRow + (4 * c + g) * kVals + 8 * u) = widen(vr, t, c, u);
     };
     // O^T: column d of keys 16 t + 4 g + r
     const T *const col = tile + (4 * g + (n >> 2)) * kRow + (n & 3) * 4;
@@ -505,7 +496,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_few(const AttnL
     T8 q[kS];
     const T *qr = q_row<T>(a, s, n);
 #pragma unroll
-    for (int c = 0; c < kS; ++c) q[c] = load_q<T>(a, qr, E4M3 ? 64 * (c / 2) + 16 * g + 8 * (c & 1) : 32 * c + 8 * g);
+    for (int c = 0; c < kS; ++c) q[c] = load_q<T>(a, qr, (4 * (8 * c / kVals) + g) * kVals + 8 * c % kVals);
 
     f32x4 o[DP / 16];
 #pragma unroll
@@ -527,16 +518,9 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_few(const AttnL
         for (int t = 0; t < 2; ++t) {
             x[t] = f32x4{0, 0, 0, 0};
 #pragma unroll
-            for (int c = 0; c < kLoads; ++c) {
-                if constexpr (E4M3) {
-                    const T4 w0 = from_e4m3<T>(kr[t][c][0]), w1 = from_e4m3<T>(kr[t][c][1]);
-                    const T4 w2 = from_e4m3<T>(kr[t][c][2]), w3 = from_e4m3<T>(kr[t][c][3]);
-                    x[t] = mfma16(__builtin_shufflevector(w0, w1, 0, 1, 2, 3, 4, 5, 6, 7), q[2 * c], x[t]);
-                    x[t] = mfma16(__builtin_shufflevector(w2, w3, 0, 1, 2, 3, 4, 5, 6, 7), q[2 * c + 1], x[t]);
-                } else {
-                    x[t] = mfma16(__builtin_bit_cast(T8, kr[t][c]), q[c], x[t]);
-                }
-            }
+            for (int c = 0; c < kLoads; ++c)
+#pragma unroll
+                for (int u = 0; u < kVals / 8; ++u) x[t] = mfma16(widen(kr, t, c, u), q[c * (kVals / 8) + u], x[t]);
         }
         if (more) load(kr, a.k_base, off);
         put_values();
@@ -692,7 +676,7 @@ constexpr int many_lds() { return KVX_TILE_KEYS * (2 * (key_row<DP>() + value_ro
 // 64-wide heads keep four waves a SIMD, 128 registers: the forms with a cap, slopes or another scale then
 // spill 16 to 18 of them (5 to 8 with a large cap), a few scratch accesses a tile.  Measured with four waves
 // and spills, an 8192-token prompt: 345 us plain, 575 capped, 530 with slopes.
-template <class T, bool E4M3, int DP, int SHAPED>
+template <class T, int CACHE, int DP, int SHAPED>
 __global__ __launch_bounds__(64 * many_waves<DP>(), DP == 64 ? 4 : DP == 128 ? 2 : 1) void attend_many(const AttnLaunch a)
 {
     typedef typename Vec<T>::x8 T8;
@@ -738,7 +722,10 @@ __global__ __launch_bounds__(64 * many_waves<DP>(), DP == 64 ? 4 : DP == 128 ? 2
     const float slack = 8.f / sc;  // a maximum that grows by less than 2^8 is not worth a rescaling
 
     // The thread's pieces of a tile: eight values of key rows krow + c * kApart.
-    typedef typename std::conditional<E4M3, u32x2, u32x4>::type Piece8;
+    struct Piece8 {
+        typename Words<cache_bytes<CACHE>(8)>::type r;
+        uint32_t e;  // mx4: the scale byte
+    };
     constexpr int kApart = 64 * kWaves / kRow;
     const int krow = threadIdx.x / kRow, chunk = threadIdx.x % kRow;
     const bool inside = chunk * 8 < a.dim;  // columns past the rows' width are zeros
@@ -748,13 +735,17 @@ __global__ __launch_bounds__(64 * many_waves<DP>(), DP == 64 ? 4 : DP == 128 ? 2
     auto load = [&](Piece8(&r)[kLoads], const uint8_t *base, int32_t i) __attribute__((always_inline)) {
 #pragma unroll
         for (int c = 0; c < kLoads; ++c) {
-            const int64_t off = offs[(i & 3) * N + krow + c * kApart] + chunk * (int)sizeof(Piece8);
-            if (inside) r[c] = *(const KVX_GLOBAL Piece8 *)(base + off);
+            const int64_t off = offs[(i & 3) * N + krow + c * kApart] + chunk * cache_bytes<CACHE>(8);
+            if (inside) {
+                r[c].r = *(const KVX_GLOBAL decltype(r[c].r) *)(base + off);
+                if constexpr (CACHE == kMx4)
+                    r[c].e = *(const KVX_GLOBAL uint8_t *)(base + off + (a.dim / 2 + chunk / 4 - chunk * 4));
+            }
         }
     };
     auto widen = [&](const Piece8 &r) __attribute__((always_inline)) {
-        if constexpr (E4M3) return __builtin_shufflevector(from_e4m3<T>(r[0]), from_e4m3<T>(r[1]), 0, 1, 2, 3, 4, 5, 6, 7);
-        else return __builtin_bit_cast(T8, r);
+        if constexpr (CACHE == kMx4) return from_mx4<T>(r.r, mx4_scale(r.e));
+        else return widen8<T, CACHE>(r.r, 0);
     };
     auto start = [&](int32_t i) __attribute__((always_inline)) { return s.walk.start(s.tile0 + i); };
     auto partly = [&](int32_t i) __attribute__((always_inline)) { return !all_see(a, s, start(i), N); };
@@ -1055,7 +1046,7 @@ __global__ __launch_bounds__(256) void join(const AttnLaunch a)
 
 // ---- launches ---------------------------------------------------------------------
 
-template <class T, bool E4M3, int DP>
+template <class T, int CACHE, int DP>
 int launch_attend_dim(const AttnLaunch &a, int which, uint32_t grid, hipStream_t stream)
 {
     // one positive scale is folded into the exponential; anything else is shaped first
@@ -1064,13 +1055,13 @@ int launch_attend_dim(const AttnLaunch &a, int which, uint32_t grid, hipStream_t
     size_t lds = 0;
     uint32_t threads = 256;
     if (which == 0) {
-        fn = plain   ? (const void *)&attend_few<T, E4M3, DP, 0>
-             : large ? (const void *)&attend_few<T, E4M3, DP, 2>
-                     : (const void *)&attend_few<T, E4M3, DP, 1>;
+        fn = plain   ? (const void *)&attend_few<T, CACHE, DP, 0>
+             : large ? (const void *)&attend_few<T, CACHE, DP, 2>
+                     : (const void *)&attend_few<T, CACHE, DP, 1>;
     } else {
-        fn = plain   ? (const void *)&attend_many<T, E4M3, DP, 0>
-             : large ? (const void *)&attend_many<T, E4M3, DP, 2>
-                     : (const void *)&attend_many<T, E4M3, DP, 1>;
+        fn = plain   ? (const void *)&attend_many<T, CACHE, DP, 0>
+             : large ? (const void *)&attend_many<T, CACHE, DP, 2>
+                     : (const void *)&attend_many<T, CACHE, DP, 1>;
         lds = many_lds<DP>();
         threads = 64 * many_waves<DP>();
         const hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
@@ -1081,19 +1072,13 @@ int launch_attend_dim(const AttnLaunch &a, int which, uint32_t grid, hipStream_t
     return (int)hipLaunchKernel(fn, dim3(grid), dim3(threads), args, lds, stream);
 }
 
-template <class T>
-int launch_attend_type(const AttnLaunch &a, int which, bool e4m3, uint32_t grid, hipStream_t stream)
+template <class T, int CACHE>
+int launch_attend_cache(const AttnLaunch &a, int which, uint32_t grid, hipStream_t stream)
 {
     switch (padded_dim(a.dim)) {
-    case 64:
-        return e4m3 ? launch_attend_dim<T, true, 64>(a, which, grid, stream)
-                    : launch_attend_dim<T, false, 64>(a, which, grid, stream);
-    case 128:
-        return e4m3 ? launch_attend_dim<T, true, 128>(a, which, grid, stream)
-                    : launch_attend_dim<T, false, 128>(a, which, grid, stream);
-    default:
-        return e4m3 ? launch_attend_dim<T, true, 256>(a, which, grid, stream)
-                    : launch_attend_dim<T, false, 256>(a, which, grid, stream);
+    case 64: return launch_attend_dim<T, CACHE, 64>(a, which, grid, stream);
+    case 128: return launch_attend_dim<T, CACHE, 128>(a, which, grid, stream);
+    default: return launch_attend_dim<T, CACHE, 256>(a, which, grid, stream);
     }
 }
 

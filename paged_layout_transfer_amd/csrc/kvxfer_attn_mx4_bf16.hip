@@ -1,0 +1,11 @@
+// kvxfer_attn_mx4_bf16.hip -- attention kernels for bfloat16 queries over 4-bit pools.
+#include "kvxfer_attn.h"
+
+namespace kvx {
+
+int launch_attend_mx4_bf16(const AttnLaunch &a, int which, uint32_t grid, hipStream_t stream)
+{
+    return launch_attend_cache<__bf16, kMx4>(a, which, grid, stream);
+}
+
+}  // namespace kvx

@@ -59,6 +59,15 @@ int launch_remap(const RemapLaunch &a, hipStream_t stream);
 // (356 us).  Below it there are more parts to join than this gains: one sequence of 32 K (8
 // tiles) 35 -> 42 us, sixteen of 200 to 5015 (10 tiles) 222 -> 213 us for four layers.
 #define KVX_ACROSS 10
+#define KVX_MX4_GROUP 32      // elements that share a scale
+#define KVX_MX4_BYTES 17      // of one group: its elements and its scale
+// The elements of a row of `bytes` bytes, as the operators see them.
+inline int64_t mx4_dim(int64_t bytes) { return bytes / KVX_MX4_BYTES * KVX_MX4_GROUP; }
+inline int32_t attn_dim(const kv_pool_desc &d, int kv_type)
+{
+    return kv_type == KV_TYPE_MX4 ? (int32_t)mx4_dim(d.head_dim) : d.head_dim;
+}
+
 #define KVX_APPEND_TOKENS 8   // new tokens of one append item
 #define KVX_APPEND_SPLIT 4    // workgroups of one append item
 // Rows joined by one workgroup.  Eight: cut prompts and turns 2 to 6 % less (91 -> 89 us), one token on 32 K
@@ -180,6 +189,54 @@ struct AttnLaunch {
     int32_t *err;
 };
 
+// A rotation, on the device: what turns pair i by one position, in 2^-64 turns.
+struct Rotation {
+    const uint64_t *turns;
+    uint32_t pairs;
+    int32_t adjacent;
+    float amplitude;
+};
+
+// Append with a rotation on the way: q and out of `attn` are the queries and where they go (null: no queries).
+struct AppendRotated {
+    AttnLaunch attn;
+    Rotation rot;
+    const int32_t *positions;  // or null: the tokens' places
+    uint32_t unit_magic, unit_shift;  // a division by the units of a row, eight elements each
+};
+
+// The new tokens' places of layers that lie one after another in `regions`, to rows.
+struct ReadLaunch {
+    AttnLaunch attn;
+    uint8_t *const *regions;  // of the first layer
+    int32_t layers;
+    void *k, *v;  // or null
+    int64_t k_layer, v_layer;  // elements; tokens' and heads' strides in attn
+    uint32_t unit_magic, unit_shift;
+};
+
+#define KVX_INLINE_SHIFTS 64  // records that ride in the kernel arguments
+#define KVX_SHIFT_TOKENS 16   // tokens of one workgroup's item
+
+struct ShiftRec {
+    const int32_t *table;
+    int32_t begin, end;  // tokens
+    int32_t delta;
+    int32_t item;  // its first item
+};
+struct ShiftLaunch {
+    uint8_t *const *regions;  // of the first layer
+    const ShiftRec *recs;     // device array, or null: inl
+    Rotation rot;
+    int64_t block_stride;
+    uint32_t tok_stride, head_stride, num_blocks, block_size, bs_magic, bs_shift;
+    int32_t dim, heads, n, layers, items;  // items of one layer
+    uint32_t unit_magic, unit_shift, head_magic, head_shift;
+    int32_t *err;
+    ShiftRec inl[KVX_INLINE_SHIFTS];
+};
+static_assert(sizeof(ShiftLaunch) <= 4096, "kernel arguments");
+
 // floor(x / d) of 0 <= x < 2^31 as a high product and a shift; d a power of two: magic 0.
 KVX_HD uint32_t div_by(uint32_t x, uint32_t magic, uint32_t shift)
 {
@@ -203,5 +260,9 @@ int padded_dim(int dim);  // 64, 128 or 256
 int launch_attend(const AttnLaunch &a, int which, int q_type, int kv_type, uint32_t grid, hipStream_t stream);
 int launch_join(const AttnLaunch &a, int q_type, uint32_t grid, hipStream_t stream);
 int launch_append(const AttnLaunch &a, int q_type, int kv_type, uint32_t grid, hipStream_t stream);
+int launch_append_mx4(const AttnLaunch &a, int q_type, uint32_t grid, hipStream_t stream);
+int launch_append_rotated(const AppendRotated &a, int q_type, int kv_type, uint32_t grid, hipStream_t stream);
+int launch_read(const ReadLaunch &a, int q_type, int kv_type, uint32_t grid, hipStream_t stream);
+int launch_shift(const ShiftLaunch &a, int kv_type, hipStream_t stream);
 
 }  // namespace kvx

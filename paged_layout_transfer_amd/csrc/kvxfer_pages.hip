@@ -214,6 +214,7 @@ __global__ __launch_bounds__(kThreads) void append_tokens(const AttnLaunch a)
 
 int launch_append(const AttnLaunch &a, int q_type, int kv_type, uint32_t grid, hipStream_t stream)
 {
+    if (kv_type == KV_TYPE_MX4) return launch_append_mx4(a, q_type, grid, stream);
     AttnLaunch arg = a;
     void *args[] = {&arg};
     const bool e4m3 = kv_type == KV_TYPE_E4M3;

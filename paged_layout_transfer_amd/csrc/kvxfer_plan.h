@@ -41,8 +41,9 @@ inline PlanLimits plan_limits(const kv_pool_desc &d, const kv_attn_desc &a)
     l.window = a.window;
     l.full = (a.flags & KV_ATTN_FULL) != 0;
     l.token_major = d.page_layout == KV_PAGE_TOKEN_MAJOR;
-    l.rows_many = rows_many(d.head_dim);
-    l.slots_few = slots_few(d.head_dim);
+    const int32_t dim = attn_dim(d, a.kv_type);
+    l.rows_many = rows_many(dim);
+    l.slots_few = slots_few(dim);
     const int64_t rows = a.max_tokens * l.group;
     const int64_t seqs = std::min<int64_t>(a.max_seqs, a.max_tokens);
     auto slices = [](int64_t n) { return (n + KVX_JOIN_ROWS - 1) / KVX_JOIN_ROWS; };

@@ -75,6 +75,12 @@ _sig("kv_attn_plan_destroy", ctypes.c_int, _P)
 _sig("kv_attn_plan_set", ctypes.c_int, _P, ctypes.POINTER(kv_seq), _I32, _P)
 _sig("kv_append_tokens", ctypes.c_int, _P, _I32, ctypes.POINTER(kv_append_args), _P)
 _sig("kv_attend", ctypes.c_int, _P, _I32, ctypes.POINTER(kv_attend_args), _P)
+_sig("kv_mx4_row_bytes", ctypes.c_int, _I32, _I32, ctypes.POINTER(_I32))
+_sig("kv_rotation_create", ctypes.c_int, ctypes.POINTER(kv_rotation_desc), ctypes.POINTER(_P))
+_sig("kv_rotation_destroy", ctypes.c_int, _P)
+_sig("kv_append_rotated", ctypes.c_int, _P, _I32, _P, ctypes.POINTER(kv_rotate_args), ctypes.POINTER(kv_append_args), _P)
+_sig("kv_read_tokens", ctypes.c_int, _P, _I32, _I32, ctypes.POINTER(kv_read_args), _P)
+_sig("kv_rotate_cached", ctypes.c_int, _P, _P, _I32, ctypes.POINTER(kv_shift), _I32, _I32, _I32, _P)
 _sig("kv_pool_get_error", ctypes.c_int, _P, _P, ctypes.POINTER(_I32))
 _sig("kv_pool_timing_start", ctypes.c_int, _P)
 _sig("kv_pool_timing_read", ctypes.c_int, _P, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_I64))
@@ -96,7 +102,8 @@ EXPORTED = ("kv_pool_create", "kv_pool_destroy", "kv_pool_alloc_blocks", "kv_poo
             "kv_gather_chunks_dma", "kv_scatter_chunks_dma",
             "kv_pool_share_blocks", "kv_pool_block_refs", "kv_pool_fork_blocks", "kv_pool_plan_compact",
             "kv_copy_pages", "kv_remap_tables", "kv_attn_plan_create", "kv_attn_plan_destroy", "kv_attn_plan_set",
-            "kv_append_tokens", "kv_attend",
+            "kv_append_tokens", "kv_attend", "kv_mx4_row_bytes", "kv_rotation_create", "kv_rotation_destroy",
+            "kv_append_rotated", "kv_read_tokens", "kv_rotate_cached",
             "kv_pool_get_error", "kv_pool_timing_start",
             "kv_pool_timing_read", "kv_pool_timing_read_each", "kv_ring_create", "kv_ring_slot", "kv_ring_destroy",
             "kv_ring_record", "kv_ring_wait", "kv_ring_stream_wait",
@@ -279,6 +286,38 @@ def kv_append_tokens(plan: int, layer: int, args: kv_append_args, stream=None) -
 
 def kv_attend(plan: int, layer: int, args: kv_attend_args, stream=None) -> None:
     _check(_lib.kv_attend(plan, layer, ctypes.byref(args), _stream(stream)), "kv_attend")
+
+
+def kv_mx4_row_bytes(head_dim: int, num_heads: int) -> int:
+    n = ctypes.c_int32()
+    _check(_lib.kv_mx4_row_bytes(head_dim, num_heads, ctypes.byref(n)), "kv_mx4_row_bytes")
+    return n.value
+
+
+def kv_rotation_create(desc: kv_rotation_desc) -> int:
+    h = ctypes.c_void_p()
+    _check(_lib.kv_rotation_create(ctypes.byref(desc), ctypes.byref(h)), "kv_rotation_create")
+    return h.value
+
+
+def kv_rotation_destroy(rotation: int) -> None:
+    _check(_lib.kv_rotation_destroy(rotation), "kv_rotation_destroy")
+
+
+def kv_append_rotated(plan: int, layer: int, rotation: int, rotate: kv_rotate_args, args: kv_append_args,
+                      stream=None) -> None:
+    _check(_lib.kv_append_rotated(plan, layer, rotation, ctypes.byref(rotate), ctypes.byref(args), _stream(stream)),
+           "kv_append_rotated")
+
+
+def kv_read_tokens(plan: int, layer_begin: int, layer_end: int, args: kv_read_args, stream=None) -> None:
+    _check(_lib.kv_read_tokens(plan, layer_begin, layer_end, ctypes.byref(args), _stream(stream)), "kv_read_tokens")
+
+
+def kv_rotate_cached(pool: int, rotation: int, kv_type: int, shifts, layer_begin: int, layer_end: int,
+                     stream=None) -> None:
+    _check(_lib.kv_rotate_cached(pool, rotation, kv_type, shifts, _nspans(shifts), layer_begin, layer_end,
+                                 _stream(stream)), "kv_rotate_cached")
 
 
 def kv_pool_get_error(pool: int, stream=None) -> int:
