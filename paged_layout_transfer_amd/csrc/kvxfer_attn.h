@@ -176,6 +176,14 @@ __device__ __forceinline__ float max_of_halves(float x)
     return fmaxf(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
 }
 
+// And of the lane 16 away.
+__device__ __forceinline__ float max_of_quarters(float x)
+{
+    const uint32_t u = __builtin_bit_cast(uint32_t, x);
+    const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    return fmaxf(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
+}
+
 // The keys one query sees, as two stretches: [0, prefix) and [low, high].  Compared without
 // branches: a mask is three compares and a select.  (With short-circuit branches beside the capped score's code
 // one of four fully masked scores was kept; the cause was not found.)
@@ -360,6 +368,67 @@ __device__ __forceinline__ void store_lse(const AttnLaunch &a, int64_t row, int3
 
 // ---- few rows: single tokens and drafts ----------------------------------------
 
+struct RowPlace {
+    int32_t token, head;
+};
+
+// The end of a few-rows kernel: the waves' maxima (m, and `mine` with the scale in base 2), sums and results, joined in
+// shared memory and stored.
+// row_of(r) is the token of the piece and the query head of row r of n_rows.
+template <class T, int DP, int SLICE, class RowOf>
+__device__ __forceinline__ void finish_few(const AttnLaunch &a, const Piece &s, bool across, int n_rows, RowOf row_of, char *shared,
+                                           float (&join_m)[4][16], float (&join_l)[4][16], float m, float mine, float l,
+                                           const f32x4 (&o)[DP / 16])
+{
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int n = lane & 15, g = lane >> 4;
+    float *const slice = (float *)(shared + wave * SLICE);
+    // join the four waves: their slices hold 16 rows of 32-bit results.  With a head to each wave
+    // there is nothing to join, and a wave reads its own slice back, a row at a time.
+    if (g == 0) join_m[wave][n] = mine, join_l[wave][n] = l;
+    __syncthreads();  // the slices' values are no longer needed
+    float top = mine;
+    if (!across) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) top = fmaxf(top, join_m[w][n]);
+    }
+    const float by = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mine - top);
+#pragma unroll
+    for (int d = 0; d < DP / 16; ++d) *(f32x4 *)(slice + n * DP + d * 16 + 4 * g) = o[d] * keep(by);
+    __syncthreads();
+    const int at = across ? lane : (int)threadIdx.x, wide = across ? 4 : 16;  // threads of a row
+    const int row = at / wide, w0 = across ? wave : 0, w1 = across ? wave + 1 : 4;
+    if (row >= n_rows) return;
+    const auto [t_r, head] = row_of(row);
+    const int64_t to_row = (int64_t)s.q_begin + t_r;
+    float sum = 0.f;
+    top = -INFINITY;
+    for (int w = w0; w < w1; ++w) top = fmaxf(top, join_m[w][row]);
+    for (int w = w0; w < w1; ++w)
+        sum += join_l[w][row] * (join_m[w][row] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(join_m[w][row] - top));
+    for (int d = at % wide * 8; d < DP; d += wide * 8) {
+        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int w = w0; w < w1; ++w)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] += ((float *)(shared + w * SLICE))[row * DP + d + k];
+        if (s.prow >= 0) {
+            float *to = a.part_o + ((int64_t)s.prow + row) * DP + d;
+            *(f32x4 *)to = f32x4{v[0], v[1], v[2], v[3]};
+            *(f32x4 *)(to + 4) = f32x4{v[4], v[5], v[6], v[7]};
+        } else {
+            store_out<T>(a, to_row, head, d, v, sum == 0.f ? 0.f : a.v_scale / sum);
+        }
+    }
+    if (at % wide == 0) {
+        if (s.prow >= 0) {
+            a.part_ml[2 * ((int64_t)s.prow + row)] = top;
+            a.part_ml[2 * ((int64_t)s.prow + row) + 1] = sum;
+        } else {
+            store_lse(a, to_row, head, top, sum);
+        }
+    }
+}
+
 // At most 16 rows (16x16x32 products).  Four waves take the piece's 32-key steps in turn, each
 // with its own running maximum, and join at the end in shared memory; or each takes a cache head
 // (AttnItem::across).  Bound by the cache's bytes: keys go from memory to the first product's
@@ -413,7 +482,6 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_few(const AttnL
 
     struct Rows {
         Load r[2][kLoads];
-        uint32_t e[2][CACHE == kMx4 ? kLoads : 1];  // mx4: the scale bytes
     };
     Rows kr, vr;
     const int32_t i1 = s.tile1 * 2;
@@ -424,8 +492,6 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_few(const AttnL
     auto load = [&](Rows &to, const uint8_t *base, const int64_t(&off)[2]) __attribute__((always_inline)) {
         auto one = [&](int t, int c) __attribute__((always_inline)) {
             to.r[t][c] = *(const KVX_GLOBAL Load *)(base + off[t] + (4 * c + g) * kBytes);
-            if constexpr (CACHE == kMx4)
-                to.e[t][c] = *(const KVX_GLOBAL uint8_t *)(base + off[t] + (a.dim / 2 + (4 * c + g) * kVals / KVX_MX4_GROUP));
         };
         if (whole_rows) {
 #pragma unroll
@@ -438,15 +504,13 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_few(const AttnL
 #pragma unroll
                 for (int c = 0; c < kLoads; ++c) {
                     to.r[t][c] = Load{};
-                    if constexpr (CACHE == kMx4) to.e[t][c] = 0;
                     if ((4 * c + g) * kVals < a.dim) one(t, c);
                 }
         }
     };
     // values 8 u .. 8 u + 7 of a load
     auto widen = [&](const Rows &from, int t, int c, int u) __attribute__((always_inline)) {
-        if constexpr (CACHE == kMx4) return from_mx4<T>(from.r[t][c][u], mx4_scale(from.e[t][c]));
-        else return widen8<T, CACHE>(from.r[t][c], u);
+        return widen8<T, CACHE>(from.r[t][c], u);
     };
     auto put_values = [&]() __attribute__((always_inline)) {  // to shared memory, row-major
 #pragma unroll
@@ -601,53 +665,13 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_few(const AttnL
         lost.restore(o);
     }
 
-    // join the four waves: their slices hold 16 rows of 32-bit results.  With a head to each wave
-    // there is nothing to join, and a wave reads its own slice back, a row at a time.
-    const float mine = m == -INFINITY ? m : m * sc - weight_shift<T>();
-    if (g == 0) join_m[wave][n] = mine, join_l[wave][n] = l;
-    __syncthreads();  // the slices' values are no longer needed
-    float top = mine;
-    if (!across) {
-#pragma unroll
-        for (int w = 0; w < 4; ++w) top = fmaxf(top, join_m[w][n]);
-    }
-    const float by = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mine - top);
-#pragma unroll
-    for (int d = 0; d < DP / 16; ++d) *(f32x4 *)((float *)tile + n * DP + d * 16 + 4 * g) = o[d] * keep(by);
-    __syncthreads();
-    const int at = across ? lane : (int)threadIdx.x, wide = across ? 4 : 16;  // threads of a row
-    const int row = at / wide, w0 = across ? wave : 0, w1 = across ? wave + 1 : 4;
-    if (row >= s.rows) return;
-    const uint32_t Rr = (uint32_t)(s.row0 + row);
-    const int32_t t_r = (int32_t)div_by(Rr, a.group_magic, a.group_shift);
-    const int32_t head = s.head * a.group + (int32_t)Rr - t_r * a.group;
-    const int64_t to_row = (int64_t)s.q_begin + t_r;
-    float sum = 0.f;
-    top = -INFINITY;
-    for (int w = w0; w < w1; ++w) top = fmaxf(top, join_m[w][row]);
-    for (int w = w0; w < w1; ++w)
-        sum += join_l[w][row] * (join_m[w][row] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(join_m[w][row] - top));
-    for (int d = at % wide * 8; d < DP; d += wide * 8) {
-        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        for (int w = w0; w < w1; ++w)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] += ((float *)(shared + w * kSlice))[row * DP + d + k];
-        if (s.prow >= 0) {
-            float *to = a.part_o + ((int64_t)s.prow + row) * DP + d;
-            *(f32x4 *)to = f32x4{v[0], v[1], v[2], v[3]};
-            *(f32x4 *)(to + 4) = f32x4{v[4], v[5], v[6], v[7]};
-        } else {
-            store_out<T>(a, to_row, head, d, v, sum == 0.f ? 0.f : a.v_scale / sum);
-        }
-    }
-    if (at % wide == 0) {
-        if (s.prow >= 0) {
-            a.part_ml[2 * ((int64_t)s.prow + row)] = top;
-            a.part_ml[2 * ((int64_t)s.prow + row) + 1] = sum;
-        } else {
-            store_lse(a, to_row, head, top, sum);
-        }
-    }
+    auto row_of = [&](int row) __attribute__((always_inline)) {
+        const uint32_t Rr = (uint32_t)(s.row0 + row);
+        const int32_t t_r = (int32_t)div_by(Rr, a.group_magic, a.group_shift);
+        return RowPlace{t_r, s.head * a.group + (int32_t)Rr - t_r * a.group};
+    };
+    finish_few<T, DP, kSlice>(a, s, across, s.rows, row_of, shared, join_m, join_l, m,
+                              m == -INFINITY ? m : m * sc - weight_shift<T>(), l, o);
 }
 
 // ---- many rows: chunks and prompts ----------------------------------------------
@@ -985,18 +1009,17 @@ __global__ __launch_bounds__(64 * many_waves<DP>(), DP == 64 ? 4 : DP == 128 ? 2
 // One workgroup joins up to KVX_JOIN_ROWS rows of a group.  A thread takes eight columns of a
 // row over every kLanes-th part, in one pass with its own running maximum; the threads of a row then
 // add up in a fixed order, so the result does not depend on which part ended first.
-template <class T, int DP>
-__global__ __launch_bounds__(256) void join(const AttnLaunch a)
+template <class T, int DP, int ROWS>
+__device__ __forceinline__ void join_rows(const AttnLaunch &a, const AttnGroup &gr, int row0)
 {
-    constexpr int kCols = DP / 8, kLanes = 256 / (KVX_JOIN_ROWS * kCols);
+    constexpr int kCols = DP / 8, kLanes = 256 / (ROWS * kCols);
     static_assert(kLanes >= 1, "");
-    __shared__ float share_m[kLanes][KVX_JOIN_ROWS], share_l[kLanes][KVX_JOIN_ROWS];
-    __shared__ __attribute__((aligned(16))) float share_v[kLanes][KVX_JOIN_ROWS][DP];
-    const AttnGroup gr = plan_record(a.groups + blockIdx.x);
-    if ((int32_t)blockIdx.x >= plan_record(a.head).n_groups) return;
-    const int d = threadIdx.x % kCols * 8, row = threadIdx.x / kCols % KVX_JOIN_ROWS;
-    const int k0 = threadIdx.x / (kCols * KVX_JOIN_ROWS);
+    __shared__ float share_m[kLanes][ROWS], share_l[kLanes][ROWS];
+    __shared__ __attribute__((aligned(16))) float share_v[kLanes][ROWS][DP];
+    const int d = threadIdx.x % kCols * 8, row = row0 + threadIdx.x / kCols % ROWS;
+    const int k0 = threadIdx.x / (kCols * ROWS);
     const bool live = row < gr.rows;
+    if (ROWS == 1 && !live) return;
     const int64_t first = (int64_t)gr.prow + (live ? row : 0);
     float m = -INFINITY, l = 0.f, v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll 4
@@ -1017,23 +1040,25 @@ __global__ __launch_bounds__(256) void join(const AttnLaunch a)
         }
     }
     if (kLanes > 1) {
-        if (d == 0) share_m[k0][row] = m, share_l[k0][row] = l;
-        *(f32x4 *)&share_v[k0][row][d] = f32x4{v[0], v[1], v[2], v[3]};
-        *(f32x4 *)&share_v[k0][row][d + 4] = f32x4{v[4], v[5], v[6], v[7]};
+        const int at = row - row0;
+        if (d == 0) share_m[k0][at] = m, share_l[k0][at] = l;
+        *(f32x4 *)&share_v[k0][at][d] = f32x4{v[0], v[1], v[2], v[3]};
+        *(f32x4 *)&share_v[k0][at][d + 4] = f32x4{v[4], v[5], v[6], v[7]};
         __syncthreads();
         if (k0 > 0) return;
+        constexpr int kUnroll = kLanes < 8 ? kLanes : 8;
         m = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < kLanes; ++k) m = fmaxf(m, share_m[k][row]);
+        for (int k = 0; k < kLanes; ++k) m = fmaxf(m, share_m[k][at]);
         l = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = 0.f;
-#pragma unroll
+#pragma unroll kUnroll
         for (int k = 0; k < kLanes; ++k) {
-            const float by = share_m[k][row] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(share_m[k][row] - m);
-            l += share_l[k][row] * by;
+            const float by = share_m[k][at] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(share_m[k][at] - m);
+            l += share_l[k][at] * by;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += share_v[k][row][d + i] * keep(by);
+            for (int i = 0; i < 8; ++i) v[i] += share_v[k][at][d + i] * keep(by);
         }
     }
     if (!live) return;
@@ -1044,7 +1069,29 @@ __global__ __launch_bounds__(256) void join(const AttnLaunch a)
     if (d == 0) store_lse(a, (int64_t)gr.q_begin + tok, head, m, l);
 }
 
+template <class T, int DP>
+__global__ __launch_bounds__(256) void join(const AttnLaunch a)
+{
+    const AttnGroup gr = plan_record(a.groups + blockIdx.x);
+    if ((int32_t)blockIdx.x >= plan_record(a.head).n_groups) return;
+    join_rows<T, DP, KVX_JOIN_ROWS>(a, gr, 0);
+}
+
+// The same for 4-bit pools, whose many parts of long contexts are as many as other pools' but took a quarter of the
+// time: a workgroup to a row (y) where there are many to join.  256 parts of 32 rows: 5.6 us, 16 with four rows to a workgroup.
+template <class T, int DP>
+__global__ __launch_bounds__(256) void join_mx4(const AttnLaunch a)
+{
+    const AttnGroup gr = plan_record(a.groups + blockIdx.x);
+    if ((int32_t)blockIdx.x >= plan_record(a.head).n_groups) return;
+    if (gr.n_parts > KVX_JOIN_MANY) join_rows<T, DP, 1>(a, gr, blockIdx.y);
+    else if (blockIdx.y == 0) join_rows<T, DP, KVX_JOIN_ROWS>(a, gr, 0);
+}
+
 // ---- launches ---------------------------------------------------------------------
+
+template <class T, int DP, int SHAPED>
+__global__ void attend_few_mx4(const AttnLaunch a);  // kvxfer_attn_mx4.h
 
 template <class T, int CACHE, int DP>
 int launch_attend_dim(const AttnLaunch &a, int which, uint32_t grid, hipStream_t stream)
@@ -1055,9 +1102,14 @@ int launch_attend_dim(const AttnLaunch &a, int which, uint32_t grid, hipStream_t
     size_t lds = 0;
     uint32_t threads = 256;
     if (which == 0) {
-        fn = plain   ? (const void *)&attend_few<T, CACHE, DP, 0>
-             : large ? (const void *)&attend_few<T, CACHE, DP, 2>
-                     : (const void *)&attend_few<T, CACHE, DP, 1>;
+        if constexpr (CACHE == kMx4)
+            fn = plain   ? (const void *)&attend_few_mx4<T, DP, 0>
+             : large ? (const void *)&attend_few_mx4<T, DP, 2>
+                     : (const void *)&attend_few_mx4<T, DP, 1>;
+        else
+            fn = plain   ? (const void *)&attend_few<T, CACHE, DP, 0>
+                 : large ? (const void *)&attend_few<T, CACHE, DP, 2>
+                         : (const void *)&attend_few<T, CACHE, DP, 1>;
     } else {
         fn = plain   ? (const void *)&attend_many<T, CACHE, DP, 0>
              : large ? (const void *)&attend_many<T, CACHE, DP, 2>
@@ -1088,10 +1140,10 @@ int launch_join_type(const AttnLaunch &a, uint32_t grid, hipStream_t stream)
     AttnLaunch arg = a;
     void *args[] = {&arg};
     const int dp = padded_dim(a.dim);
-    const void *fn = dp == 64    ? (const void *)&join<T, 64>
-                     : dp == 128 ? (const void *)&join<T, 128>
-                                 : (const void *)&join<T, 256>;
-    return (int)hipLaunchKernel(fn, dim3(grid), dim3(256), args, 0, stream);
+    const void *fn = dp == 64    ? (a.mx4 ? (const void *)&join_mx4<T, 64> : (const void *)&join<T, 64>)
+                     : dp == 128 ? (a.mx4 ? (const void *)&join_mx4<T, 128> : (const void *)&join<T, 128>)
+                                 : (a.mx4 ? (const void *)&join_mx4<T, 256> : (const void *)&join<T, 256>);
+    return (int)hipLaunchKernel(fn, dim3(grid, a.mx4 ? KVX_JOIN_ROWS : 1), dim3(256), args, 0, stream);
 }
 
 }  // namespace kvx

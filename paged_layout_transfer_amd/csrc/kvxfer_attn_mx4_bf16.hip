@@ -1,5 +1,5 @@
 // kvxfer_attn_mx4_bf16.hip -- attention kernels for bfloat16 queries over 4-bit pools.
-#include "kvxfer_attn.h"
+#include "kvxfer_attn_mx4.h"
 
 namespace kvx {
 

@@ -1,5 +1,5 @@
 // kvxfer_attn_mx4_f16.hip -- attention kernels for half-precision queries over 4-bit pools.
-#include "kvxfer_attn.h"
+#include "kvxfer_attn_mx4.h"
 
 namespace kvx {
 

@@ -68,11 +68,33 @@ inline int32_t attn_dim(const kv_pool_desc &d, int kv_type)
     return kv_type == KV_TYPE_MX4 ? (int32_t)mx4_dim(d.head_dim) : d.head_dim;
 }
 
+// Few rows over mx4 pools, for a width padded to `dp`: the 1 KiB pieces of a wave's 32 keys that its lanes read, and their
+// space in shared memory, where the rows of each head take the place of one more.
+KVX_HD constexpr int32_t mx4_pieces(int32_t dp) { return dp == 64 ? 12 : dp == 128 ? 10 : 9; }
+KVX_HD constexpr int32_t mx4_raw(int32_t dp) { return dp == 64 ? 13312 : dp == 128 ? 10752 : 9728; }
+// The cache heads whose rows share a product's 16 columns: as many as those hold (a row of values takes whole 16-byte
+// pieces), at most most_heads, dividing the heads.
+inline int32_t mx4_pack(int32_t heads, int64_t rows, int32_t row_bytes, int32_t dp, int64_t most_heads)
+{
+    const int64_t per = (row_bytes + 15) / 16;
+    int64_t most = 2 * mx4_pieces(dp) / per;
+    if (most > mx4_raw(dp) / (33 * 16 * per)) most = mx4_raw(dp) / (33 * 16 * per);
+    if (most > KVX_ROWS_FEW / rows) most = KVX_ROWS_FEW / rows;
+    if (most > most_heads) most = most_heads;
+    int32_t n = most < heads ? (int32_t)most : heads;
+    while (n > 1 && heads % n) --n;
+    return n < 1 ? 1 : n;
+}
+// Tiles of a workgroup below which packs are made smaller, so that more workgroups work: one sequence of 128 K tokens (8
+// tiles to each of 512 workgroups with four heads) 42.4 -> 40.3 us, four layers of sixteen of 200 to 5015 (2.6) 148 -> 140.
+#define KVX_PACK_TILES 12
+
 #define KVX_APPEND_TOKENS 8   // new tokens of one append item
 #define KVX_APPEND_SPLIT 4    // workgroups of one append item
 // Rows joined by one workgroup.  Eight: cut prompts and turns 2 to 6 % less (91 -> 89 us), one token on 32 K
 // 34.5 -> 37 us, four layers of sixteen sequences 207.5 -> 210.7.
 #define KVX_JOIN_ROWS 4
+#define KVX_JOIN_MANY 16  // parts of a row from which on a workgroup joins one row of a 4-bit pool's
 
 // Rows of a piece of the many-rows kernel: 32 to a wave; at the widest heads a wave's
 // registers leave room for four waves only.
@@ -90,7 +112,9 @@ struct AttnItem {
     int32_t prow;    // first row in the workspace of partial results, or -1: the result is whole
     int16_t rows;    // rows of the piece, unless the sequence's end first
     int16_t across;  // few rows: the four waves take the cache heads head .. head + 3 instead of
-                     // every fourth step of one head; wave w's partial rows lie 16 w behind prow
+                     // every fourth step of one head; wave w's partial rows lie 16 w behind prow.  mx4 pools:
+                     // the cache heads, from `head` on, whose rows are worked on together (mx4_pack); the
+                     // partial rows of the h-th of them lie h * (rows of one head) behind prow
 };
 static_assert(sizeof(AttnItem) == 48, "");
 
@@ -168,10 +192,11 @@ struct AttnLaunch {
     uint8_t *k_base, *v_base;  // the layer's regions
     int64_t block_stride;
     uint32_t tok_stride, head_stride;  // bytes between tokens and heads of one page
+    uint32_t row;                      // bytes of one row
     uint32_t num_blocks, block_size, bs_magic, bs_shift;
     int32_t dim, heads, group;  // head_dim, cache heads, query heads to a cache head
     uint32_t group_magic, group_shift;
-    int32_t window, full;
+    int32_t window, full, mx4;
     int64_t n_tokens;
     const void *q;
     void *out;

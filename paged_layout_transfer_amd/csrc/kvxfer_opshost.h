@@ -130,6 +130,8 @@ inline int launch_base(kv_attn_plan *p, int32_t layer, kvx::AttnLaunch *a)
     a->v_base = static_cast<uint8_t *>(p->pool->bases[2 * layer + 1]);
     set_pages(d, a);
     a->dim = attn_dim(d, p->desc.kv_type);
+    a->mx4 = p->desc.kv_type == KV_TYPE_MX4;
+    a->row = (uint32_t)(d.head_dim * d.elem_bytes);
     a->heads = d.num_heads;
     a->group = p->lim.group;
     kvx::set_div((uint32_t)a->group, &a->group_magic, &a->group_shift);

@@ -19,7 +19,8 @@ constexpr int32_t kSlotsMany = 256;
 
 struct PlanLimits {
     int32_t heads, group, window, rows_many, slots_few;
-    bool full, token_major;
+    int32_t dim, row_bytes;  // of a head; row_bytes for mx4 pools only
+    bool full, token_major, mx4;
     int64_t cap_few, cap_many, cap_groups, cap_append, cap_prows;
 };
 
@@ -43,6 +44,9 @@ inline PlanLimits plan_limits(const kv_pool_desc &d, const kv_attn_desc &a)
     l.token_major = d.page_layout == KV_PAGE_TOKEN_MAJOR;
     const int32_t dim = attn_dim(d, a.kv_type);
     l.rows_many = rows_many(dim);
+    l.mx4 = a.kv_type == KV_TYPE_MX4;
+    l.row_bytes = d.head_dim;
+    l.dim = dim;
     l.slots_few = slots_few(dim);
     const int64_t rows = a.max_tokens * l.group;
     const int64_t seqs = std::min<int64_t>(a.max_seqs, a.max_tokens);
@@ -50,9 +54,10 @@ inline PlanLimits plan_limits(const kv_pool_desc &d, const kv_attn_desc &a)
     const int64_t few = seqs * l.heads, cut_few = cut_parts(few, l.slots_few);
     l.cap_few = all_parts(few, l.slots_few);
     // a cut piece has two parts or more, and one record for KVX_JOIN_ROWS of its rows
-    const int64_t heads_cut = l.heads % 4 == 0 ? 4 : 1;  // of one piece (Split::across)
+    // of one piece (Split::across, mx4_pack)
+    const int64_t heads_cut = l.mx4 ? std::min(l.heads, KVX_ROWS_FEW) : l.heads % 4 == 0 ? 4 : 1;
     l.cap_groups = std::min(cut_few / 2 * heads_cut, few) * slices(std::min<int64_t>(rows, KVX_ROWS_FEW));
-    l.cap_prows = cut_few * KVX_ROWS_FEW * heads_cut;
+    l.cap_prows = cut_few * KVX_ROWS_FEW * (l.mx4 ? 1 : heads_cut);  // the heads of a pack share their 16 rows
     l.cap_many = 0;
     if (rows > KVX_ROWS_FEW) {
         const int64_t many = (rows / l.rows_many + seqs) * l.heads, cut_many = cut_parts(many, kSlotsMany);
@@ -106,7 +111,7 @@ struct SplitCost {
 };
 // Measured in tiles of 128-wide 16-bit heads without a cap, and used for all: a 64-wide tile costs less, a capped
 // one more, and with them the costs in tiles.
-constexpr SplitCost kCostFew{2, 2, 10, 2}, kCostMany{1, 4, 4, 8}, kCostHalf{1, 4, 5, 8};
+constexpr SplitCost kCostFew{2, 2, 10, 2}, kCostFewMx4{2, 2, 10, 2}, kCostMany{1, 4, 4, 8}, kCostHalf{1, 4, 5, 8};
 // A tile with waves 0 to 3 at work takes 72 hundredths of the time of one with all (1.5 and
 // 2.1 us, 128-wide heads; 512 new tokens on 16 K cached, cut to one round either way: 217 and 155 us).
 constexpr int64_t kHalfTile = 72;
@@ -230,8 +235,50 @@ inline void cut(Plan &p, std::vector<AttnItem> &out, const PlanLimits &l, int32_
     });
 }
 
+// The same for mx4 pools' few rows, whose pieces are of one pack of heads each (AttnItem::head, across).
+inline void cut_packs(Plan &p, const PlanLimits &l, const Split &split, int64_t *prow)
+{
+    std::vector<AttnItem> &out = p.few;
+    bool same = true;  // packs of one size
+    for (const AttnItem &it : p.whole) {
+        same &= it.across == p.whole[0].across;
+        const int64_t n = (it.tile1 + split.share - 1) / split.share;
+        const int32_t rows = it.q_len * l.group;
+        AttnItem part = it;
+        if (n <= 1) {
+            out.push_back(part);
+            continue;
+        }
+        for (int32_t h = 0; h < it.across; ++h)
+            for (int32_t r = 0; r < rows; r += KVX_JOIN_ROWS)
+                p.groups.push_back(AttnGroup{(int32_t)(*prow + h * rows + r), (int32_t)n, KVX_ROWS_FEW,
+                                             std::min(KVX_JOIN_ROWS, rows - r), it.q_begin, it.q_len, it.head + h, r});
+        for (int64_t k = 0; k < n; ++k) {
+            part.tile0 = (int32_t)(it.tile1 * k / n);
+            part.tile1 = (int32_t)(it.tile1 * (k + 1) / n);
+            part.prow = (int32_t)(*prow + k * KVX_ROWS_FEW);
+            out.push_back(part);
+        }
+        *prow += n * KVX_ROWS_FEW;
+    }
+    // longest first; the packs of one stretch of keys side by side
+    std::stable_sort(out.begin(), out.end(), [](const AttnItem &a, const AttnItem &b) {
+        const int32_t x = a.tile1 - a.tile0, y = b.tile1 - b.tile0;
+        return x != y ? x > y : a.q_begin != b.q_begin ? a.q_begin < b.q_begin : a.tile0 < b.tile0;
+    });
+    // and on one chiplet (workgroup b runs on chiplet b mod 8), whose cache then gives the lines where two packs of a
+    // token meet to both of them
+    const size_t units = same && !out.empty() ? (size_t)(l.heads / out[0].across) : 1;
+    if (units > 1) {
+        p.whole.assign(out.begin(), out.end());
+        for (size_t b = 0; b + 8 * units <= out.size(); b += 8 * units)
+            for (size_t k = 0; k < 8 * units; ++k) out[b + k] = p.whole[b + k % 8 * units + k / 8];
+    }
+}
+
 // The pieces of the few rows' or the many rows' sequences into `whole`, `step` rows each; the largest's rows.
-inline int32_t pieces_of(Plan &p, const PlanLimits &l, const kv_seq *seqs, int32_t n, bool few, int32_t step)
+inline int32_t pieces_of(Plan &p, const PlanLimits &l, const kv_seq *seqs, int32_t n, bool few, int32_t step,
+                         int64_t most_heads = KVX_ROWS_FEW)
 {
     int32_t most = 0;
     p.whole.clear();
@@ -255,7 +302,12 @@ inline int32_t pieces_of(Plan &p, const PlanLimits &l, const kv_seq *seqs, int32
             it.tile1 = w.n_tiles;
             it.prow = -1;
             it.rows = (int16_t)step;
-            p.whole.push_back(it);
+            if (!few || !l.mx4) {
+                p.whole.push_back(it);
+                continue;
+            }
+            it.across = (int16_t)mx4_pack(l.heads, rows, l.row_bytes, l.dim <= 64 ? 64 : l.dim <= 128 ? 128 : 256, most_heads);
+            for (it.head = 0; it.head < l.heads; it.head += it.across) p.whole.push_back(it);
         }
     }
     return most;
@@ -271,8 +323,20 @@ inline void build_plan(Plan &p, const PlanLimits &l, const kv_seq *seqs, int32_t
     p.tokens_end = 0;
     p.appendable = true;
     int64_t prow = 0;
-    if (pieces_of(p, l, seqs, n, true, KVX_ROWS_FEW) > 0)
-        cut(p, p.few, l, KVX_ROWS_FEW, choose_split(p, l, l.slots_few, kCostFew, true), &prow);
+    if (pieces_of(p, l, seqs, n, true, KVX_ROWS_FEW) > 0) {
+        if (l.mx4) {
+            // packs of fewer heads where larger ones do not give every workgroup KVX_PACK_TILES
+            int64_t tiles = 0;
+            for (const AttnItem &it : p.whole) tiles += (int64_t)it.tile1 * it.across;
+            const int64_t most = tiles / ((int64_t)KVX_PACK_TILES * l.slots_few);
+            if (most < KVX_ROWS_FEW) (void)pieces_of(p, l, seqs, n, true, KVX_ROWS_FEW, std::max<int64_t>(1, most));
+            PlanLimits packs = l;  // a piece for each already
+            packs.heads = 1;
+            cut_packs(p, l, choose_split(p, packs, l.slots_few, kCostFewMx4, true), &prow);
+        } else {
+            cut(p, p.few, l, KVX_ROWS_FEW, choose_split(p, l, l.slots_few, kCostFew, true), &prow);
+        }
+    }
     int32_t step = l.rows_many;
     if (const int32_t rows = pieces_of(p, l, seqs, n, false, step)) {
         Split split = choose_split(p, l, kSlotsMany, kCostMany, false);

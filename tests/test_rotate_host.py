@@ -136,3 +136,21 @@ def test_the_reference_rounds_to_nearest():
     assert torch.allclose(c[:3], torch.cos(torch.tensor([[0.0], [1], [-3]]).double() * torch.tensor([1.0, 0.25, 2.0 ** -40]).double()),
                           rtol=0, atol=1e-15)
     assert torch.allclose(c * c + s * s, torch.ones_like(c), rtol=0, atol=1e-15)
+
+
+def test_plans_over_4_bit_pools_walk_every_visible_key_once(tmp_path):
+    """tests/plan_walk_mx4.cpp under AddressSanitizer and UBSan (host code only)."""
+    import os
+    import subprocess
+
+    from paged_layout_transfer_amd import _build
+
+    rocm = os.path.dirname(os.path.dirname(os.path.realpath(_build.HIPCC)))
+    out = str(tmp_path / "plan_walk_mx4")
+    subprocess.run(["g++", "-std=c++17", "-O2", "-g", "-Wall", "-fsanitize=address,undefined",
+                    "-fno-sanitize-recover=undefined", "-D__HIP_PLATFORM_AMD__", "-I", os.path.join(rocm, "include"),
+                    "-I", os.path.join(_build.ROOT, "include"), "-I", _build.CSRC,
+                    os.path.join(os.path.dirname(__file__), "plan_walk_mx4.cpp"), "-o", out],
+                   check=True, capture_output=True)
+    r = subprocess.run([out], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout[-1000:] + r.stderr[-2000:]
