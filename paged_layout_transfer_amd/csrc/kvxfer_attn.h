@@ -1077,15 +1077,16 @@ __global__ __launch_bounds__(256) void join(const AttnLaunch a)
     join_rows<T, DP, KVX_JOIN_ROWS>(a, gr, 0);
 }
 
-// The same for 4-bit pools, whose many parts of long contexts are as many as other pools' but took a quarter of the
-// time: a workgroup to a row (y) where there are many to join.  256 parts of 32 rows: 5.6 us, 16 with four rows to a workgroup.
+// The same for 4-bit pools, whose long contexts have as many parts as other pools' but took a quarter of the time: where
+// there are more than KVX_JOIN_MANY, a record holds one row and all of a workgroup's threads take it.  256 parts of 32 rows: 6.5
+// us, 16 to 22 with four rows to a workgroup.
 template <class T, int DP>
 __global__ __launch_bounds__(256) void join_mx4(const AttnLaunch a)
 {
     const AttnGroup gr = plan_record(a.groups + blockIdx.x);
     if ((int32_t)blockIdx.x >= plan_record(a.head).n_groups) return;
-    if (gr.n_parts > KVX_JOIN_MANY) join_rows<T, DP, 1>(a, gr, blockIdx.y);
-    else if (blockIdx.y == 0) join_rows<T, DP, KVX_JOIN_ROWS>(a, gr, 0);
+    if (gr.n_parts > KVX_JOIN_MANY && gr.rows == 1) join_rows<T, DP, 1>(a, gr, 0);
+    else join_rows<T, DP, KVX_JOIN_ROWS>(a, gr, 0);
 }
 
 // ---- launches ---------------------------------------------------------------------
@@ -1143,7 +1144,7 @@ int launch_join_type(const AttnLaunch &a, uint32_t grid, hipStream_t stream)
     const void *fn = dp == 64    ? (a.mx4 ? (const void *)&join_mx4<T, 64> : (const void *)&join<T, 64>)
                      : dp == 128 ? (a.mx4 ? (const void *)&join_mx4<T, 128> : (const void *)&join<T, 128>)
                                  : (a.mx4 ? (const void *)&join_mx4<T, 256> : (const void *)&join<T, 256>);
-    return (int)hipLaunchKernel(fn, dim3(grid, a.mx4 ? KVX_JOIN_ROWS : 1), dim3(256), args, 0, stream);
+    return (int)hipLaunchKernel(fn, dim3(grid), dim3(256), args, 0, stream);
 }
 
 }  // namespace kvx

@@ -91,10 +91,11 @@ inline int32_t mx4_pack(int32_t heads, int64_t rows, int32_t row_bytes, int32_t 
 
 #define KVX_APPEND_TOKENS 8   // new tokens of one append item
 #define KVX_APPEND_SPLIT 4    // workgroups of one append item
+#define KVX_FEW_UNITS 128     // a token's units up to which one workgroup takes a whole item (rotated appends, reads)
 // Rows joined by one workgroup.  Eight: cut prompts and turns 2 to 6 % less (91 -> 89 us), one token on 32 K
 // 34.5 -> 37 us, four layers of sixteen sequences 207.5 -> 210.7.
 #define KVX_JOIN_ROWS 4
-#define KVX_JOIN_MANY 16  // parts of a row from which on a workgroup joins one row of a 4-bit pool's
+#define KVX_JOIN_MANY 16  // parts beyond which a workgroup joins one row of a 4-bit pool's results
 
 // Rows of a piece of the many-rows kernel: 32 to a wave; at the widest heads a wave's
 // registers leave room for four waves only.
@@ -227,7 +228,9 @@ struct AppendRotated {
     AttnLaunch attn;
     Rotation rot;
     const int32_t *positions;  // or null: the tokens' places
-    uint32_t unit_magic, unit_shift;  // a division by the units of a row, eight elements each
+    uint32_t lg_split;         // 2^lg_split workgroups to an item
+    // divisions by the units of a row, of a token, by the pairs, and by the eights of an mx4 row and of a token's k and v
+    uint32_t unit_magic, unit_shift, all_magic, all_shift, pair_magic, pair_shift, eight_magic, eight_shift, each_magic, each_shift;
 };
 
 // The new tokens' places of layers that lie one after another in `regions`, to rows.
@@ -237,11 +240,18 @@ struct ReadLaunch {
     int32_t layers;
     void *k, *v;  // or null
     int64_t k_layer, v_layer;  // elements; tokens' and heads' strides in attn
-    uint32_t unit_magic, unit_shift;
+    uint32_t lg_split, unit_magic, unit_shift, all_magic, all_shift;
+    int32_t deep;  // layers of a workgroup
 };
 
 #define KVX_INLINE_SHIFTS 64  // records that ride in the kernel arguments
+#define KVX_READ_DEEP 4       // layers that a workgroup reads (32 of 2860 tokens of 2 heads: 13.9 us with 1, 11.7, 12.9 with 16)
 #define KVX_SHIFT_TOKENS 16   // tokens of one workgroup's item
+// Units of work of a thread for which a workgroup takes more layers: of 2 heads' mx4 rows, two units to a thread and layer,
+// four layers (30.1 us with one, 25.0 with two, 23.2 with four or eight); of 8 heads' 16-bit rows, four, two (232 us
+// with one, 233 with two, 238 with four, 256 with eight).
+#define KVX_SHIFT_UNITS 8
+#define KVX_DEEP_GROUPS 1024  // workgroups that remain where one takes more than a layer
 
 struct ShiftRec {
     const int32_t *table;
@@ -256,6 +266,7 @@ struct ShiftLaunch {
     int64_t block_stride;
     uint32_t tok_stride, head_stride, num_blocks, block_size, bs_magic, bs_shift;
     int32_t dim, heads, n, layers, items;  // items of one layer
+    int32_t deep;                          // layers of a workgroup
     uint32_t unit_magic, unit_shift, head_magic, head_shift;
     int32_t *err;
     ShiftRec inl[KVX_INLINE_SHIFTS];

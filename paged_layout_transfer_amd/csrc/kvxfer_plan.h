@@ -56,7 +56,8 @@ inline PlanLimits plan_limits(const kv_pool_desc &d, const kv_attn_desc &a)
     // a cut piece has two parts or more, and one record for KVX_JOIN_ROWS of its rows
     // of one piece (Split::across, mx4_pack)
     const int64_t heads_cut = l.mx4 ? std::min(l.heads, KVX_ROWS_FEW) : l.heads % 4 == 0 ? 4 : 1;
-    l.cap_groups = std::min(cut_few / 2 * heads_cut, few) * slices(std::min<int64_t>(rows, KVX_ROWS_FEW));
+    l.cap_groups = std::min(cut_few / 2 * heads_cut, few) *
+                   (l.mx4 ? std::min<int64_t>(rows, KVX_ROWS_FEW) : slices(std::min<int64_t>(rows, KVX_ROWS_FEW)));
     l.cap_prows = cut_few * KVX_ROWS_FEW * (l.mx4 ? 1 : heads_cut);  // the heads of a pack share their 16 rows
     l.cap_many = 0;
     if (rows > KVX_ROWS_FEW) {
@@ -249,10 +250,11 @@ inline void cut_packs(Plan &p, const PlanLimits &l, const Split &split, int64_t 
             out.push_back(part);
             continue;
         }
+        const int32_t each = n > KVX_JOIN_MANY ? 1 : KVX_JOIN_ROWS;
         for (int32_t h = 0; h < it.across; ++h)
-            for (int32_t r = 0; r < rows; r += KVX_JOIN_ROWS)
+            for (int32_t r = 0; r < rows; r += each)
                 p.groups.push_back(AttnGroup{(int32_t)(*prow + h * rows + r), (int32_t)n, KVX_ROWS_FEW,
-                                             std::min(KVX_JOIN_ROWS, rows - r), it.q_begin, it.q_len, it.head + h, r});
+                                             std::min(each, rows - r), it.q_begin, it.q_len, it.head + h, r});
         for (int64_t k = 0; k < n; ++k) {
             part.tile0 = (int32_t)(it.tile1 * k / n);
             part.tile1 = (int32_t)(it.tile1 * (k + 1) / n);
@@ -330,9 +332,18 @@ inline void build_plan(Plan &p, const PlanLimits &l, const kv_seq *seqs, int32_t
             for (const AttnItem &it : p.whole) tiles += (int64_t)it.tile1 * it.across;
             const int64_t most = tiles / ((int64_t)KVX_PACK_TILES * l.slots_few);
             if (most < KVX_ROWS_FEW) (void)pieces_of(p, l, seqs, n, true, KVX_ROWS_FEW, std::max<int64_t>(1, most));
-            PlanLimits packs = l;  // a piece for each already
-            packs.heads = 1;
-            cut_packs(p, l, choose_split(p, packs, l.slots_few, kCostFewMx4, true), &prow);
+            // The split is chosen with a piece for each pack, or, where all packs are of one size, for each sequence's first
+            // and as many heads as packs (a plan of 16 sequences: 234 us of the host, 40).
+            const int32_t across = p.whole[0].across;
+            const bool same = std::all_of(p.whole.begin(), p.whole.end(), [&](const AttnItem &it) { return it.across == across; });
+            PlanLimits packs = l;
+            packs.heads = same ? l.heads / across : 1;
+            packs.token_major = false;
+            if (same)
+                p.whole.erase(std::remove_if(p.whole.begin(), p.whole.end(), [](const AttnItem &it) { return it.head; }), p.whole.end());
+            const Split split = choose_split(p, packs, l.slots_few, kCostFewMx4, true);
+            if (same) (void)pieces_of(p, l, seqs, n, true, KVX_ROWS_FEW, std::max<int64_t>(1, most));
+            cut_packs(p, l, split, &prow);
         } else {
             cut(p, p.few, l, KVX_ROWS_FEW, choose_split(p, l, l.slots_few, kCostFew, true), &prow);
         }

@@ -13,6 +13,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "kvxfer_device.h"
 
@@ -86,27 +87,29 @@ __device__ __forceinline__ uint64_t turns_of(const Rotation &r, int32_t pos, uin
 
 // ---- heads -------------------------------------------------------------------
 
-// A row is worked on in units of eight elements: two runs of four, so that a unit holds whole pairs.  Unit j of
-// paired halves holds elements 4j .. and their partners pairs + 4j ..; behind the pairs, and of neighbours paired, 8j .. 8j + 7.
-template <bool ADJACENT>
+// A row is worked on in units of two runs of VEC elements, so that a unit holds whole pairs: 8, 16 bytes of a 16-bit row
+// each, where the pairs are a multiple of 8 and the row one of 16, else 4.  Unit j of paired halves holds elements VEC j ..
+// and their partners pairs + VEC j ..; behind the pairs, and of neighbours paired, 2 VEC j .. 2 VEC j + 2 VEC - 1.
+template <bool ADJACENT, int VEC>
 struct Unit {
     uint32_t a, b;  // first element of either run
     bool turns;
     __device__ __forceinline__ Unit(uint32_t j, uint32_t pairs)
     {
-        turns = j < pairs / 4;
-        a = !ADJACENT && turns ? 4 * j : 8 * j;
-        b = !ADJACENT && turns ? pairs + 4 * j : 8 * j + 4;
+        turns = j < pairs / VEC;
+        a = !ADJACENT && turns ? VEC * j : 2 * VEC * j;
+        b = !ADJACENT && turns ? pairs + VEC * j : 2 * VEC * j + VEC;
     }
 };
+inline int unit_vec(uint32_t pairs, int32_t dim) { return pairs % 8 == 0 && dim % 16 == 0 ? 8 : 4; }
 
-// Eight values of a unit turned; cs holds the four pairs from the unit's first on.
-template <bool ADJACENT>
-__device__ __forceinline__ void turn_unit(float (&x)[8], const float2 *cs)
+// The values of a unit turned; cs holds its pairs.
+template <bool ADJACENT, int VEC>
+__device__ __forceinline__ void turn_unit(float (&x)[2 * VEC], const float2 *cs)
 {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float &u = x[ADJACENT ? 2 * i : i], &v = x[ADJACENT ? 2 * i + 1 : i + 4];
+    for (int i = 0; i < VEC; ++i) {
+        float &u = x[ADJACENT ? 2 * i : i], &v = x[ADJACENT ? 2 * i + 1 : i + VEC];
         const float c = cs[i].x, s = cs[i].y, y = u;
         u = __builtin_fmaf(y, c, -(v * s));
         v = __builtin_fmaf(y, s, v * c);
@@ -159,20 +162,31 @@ __device__ __forceinline__ uint32_t partner(uint32_t e, uint32_t pairs)
     return e < pairs ? e + pairs : e < 2 * pairs ? e - pairs : e;
 }
 
-template <class T>
-__device__ __forceinline__ void load4(float *x, const T *p)
+// A run of elements: as it lies in memory, as values, and back.
+template <class E, int N>
+struct Run {
+    typedef E type __attribute__((ext_vector_type(N)));
+};
+template <class T, int N>
+__device__ __forceinline__ void values_of(float *x, typename Run<T, N>::type v)
 {
-    const typename Vec<T>::x4 v = *(const typename Vec<T>::x4 *)p;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = (float)v[i];
+    for (int i = 0; i < N; ++i) x[i] = (float)v[i];
 }
-template <class T>
-__device__ __forceinline__ void store4(T *p, const float *x)
+template <class T, int N>
+__device__ __forceinline__ typename Run<T, N>::type run_of(const float *x)
 {
-    typename Vec<T>::x4 v;
+    typename Run<T, N>::type v;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = (T)x[i];
-    *(typename Vec<T>::x4 *)p = v;
+    for (int i = 0; i < N; ++i) v[i] = (T)x[i];
+    return v;
+}
+
+// A store of what no one reads soon enough to find it in a cache of 4 MB.
+template <class E, class V>
+__device__ __forceinline__ void store_past(E *to, V v)
+{
+    __builtin_nontemporal_store(v, (V *)to);
 }
 
 // x / scale in 32 bits (correctly rounded), clamped to +-448; NaN passes by the bounds.
@@ -181,138 +195,283 @@ __device__ __forceinline__ float e4m3_of(float x, float scale)
     const float y = x / scale;
     return y != y ? y : fminf(fmaxf(y, -448.f), 448.f);
 }
-__device__ __forceinline__ uint32_t to_e4m3(const float *x, float scale)
+__device__ __forceinline__ uint32_t to_e4m3_word(const float *x, float scale)
 {
     int p = __builtin_amdgcn_cvt_pk_fp8_f32(e4m3_of(x[0], scale), e4m3_of(x[1], scale), 0, false);
     return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(e4m3_of(x[2], scale), e4m3_of(x[3], scale), p, true);
 }
 
-// ---- append with a rotation on the way --------------------------------------------
-
-// Four workgroups to an item, two of its tokens each, and as many along y as a token's units (keys, values, then
-// queries) take 256 threads: a thread owns one unit of both tokens.
-template <class T, int CACHE, bool ADJACENT>
-__global__ __launch_bounds__(kThreads) void append_rotated(const AppendRotated x)
+template <int N>
+__device__ __forceinline__ typename Run<uint8_t, N>::type to_e4m3(const float *x, float scale)
 {
-    constexpr int kBatch = KVX_APPEND_TOKENS / KVX_APPEND_SPLIT;
-    constexpr bool MX4 = CACHE == kMx4;
-    __shared__ float2 cs[kBatch][kMaxPairs];
-    __shared__ double2 cs64[MX4 ? kBatch : 1][MX4 ? kMaxPairs : 1];
-    const AttnLaunch &a = x.attn;
-    const AppendItem it = plan_record(a.append + blockIdx.x / KVX_APPEND_SPLIT);
-    if ((int32_t)(blockIdx.x / KVX_APPEND_SPLIT) >= plan_record(a.head).n_append) return;
-    const uint32_t begin = blockIdx.x % KVX_APPEND_SPLIT * kBatch;
-    if (begin >= (uint32_t)it.count) return;
-    const uint32_t count = min((uint32_t)it.count - begin, (uint32_t)kBatch), pairs = x.rot.pairs;
-    const int64_t row0 = (int64_t)it.row + begin;
-    const uint32_t pos0 = (uint32_t)it.pos + begin;
-    const uint32_t units = (uint32_t)a.dim / 8, kv = units * (uint32_t)a.heads;
-    const uint32_t all = 2 * kv + (a.q ? kv * (uint32_t)a.group : 0);
-
-    const bool wide = MX4 && blockIdx.y * kThreads < kv;  // keys are among the units
-    for (uint32_t i = threadIdx.x; i < count * pairs; i += kThreads) {
-        const uint32_t u = i >= pairs, pair = i - u * pairs;
-        if (row0 + u >= a.n_tokens) continue;
-        const int32_t pos = x.positions ? x.positions[row0 + u] : (int32_t)(pos0 + u);
-        const uint64_t t = turns_of(x.rot, pos, pair);
-        cs[u][pair] = turn32(t, x.rot.amplitude);
-        if constexpr (MX4) {
-            if (wide) cs64[u][pair] = turn64(t, x.rot.amplitude);
-        }
-    }
-    __syncthreads();
-
-    for (uint32_t c = blockIdx.y * kThreads + threadIdx.x; c < all; c += gridDim.y * kThreads) {
-        const bool key = c < kv, query = c >= 2 * kv;
-        const uint32_t hc = key ? c : query ? c - 2 * kv : c - kv;
-        const uint32_t h = div_by(hc, x.unit_magic, x.unit_shift), j = hc - h * units;
-        if (query) {
-            const Unit<ADJACENT> unit(j, pairs);
+    uint32_t w[N / 4];
 #pragma unroll
-            for (uint32_t u = 0; u < kBatch; ++u) {
-                const int64_t row = row0 + u;
-                if (u >= count || row >= a.n_tokens) continue;
-                const T *from = (const T *)a.q + row * a.q_token + (int64_t)h * a.q_head;
-                T *to = (T *)a.out + row * a.out_token + (int64_t)h * a.out_head;
-                float v[8];
-                load4(v, from + unit.a);
-                load4(v + 4, from + unit.b);
-                if (unit.turns) turn_unit<ADJACENT>(v, &cs[u][4 * j]);
-                store4(to + unit.a, v);
-                store4(to + unit.b, v + 4);
-            }
-            continue;
-        }
-        const T *src = key ? (const T *)a.k_new + (int64_t)h * a.k_head : (const T *)a.v_new + (int64_t)h * a.v_head;
-        const int64_t src_tok = key ? a.k_token : a.v_token;
-        uint8_t *base = (key ? a.k_base : a.v_base) + (int64_t)h * a.head_stride;
-        const float scale = key ? a.k_scale : a.v_scale;
+    for (int i = 0; i < N / 4; ++i) w[i] = to_e4m3_word(x + 4 * i, scale);
+    return __builtin_bit_cast(typename Run<uint8_t, N>::type, w);
+}
+template <int N>
+__device__ __forceinline__ void values_of_e4m3(float *x, typename Run<uint8_t, N>::type v)
+{
 #pragma unroll
-        for (uint32_t u = 0; u < kBatch; ++u) {
-            const int64_t row = row0 + u;
-            if (u >= count || row >= a.n_tokens) continue;
-            const uint32_t pos = pos0 + u, page = div_by(pos, a.bs_magic, a.bs_shift);
-            const int32_t blk = it.table[page];
-            const T *from = src + row * src_tok;
-            if ((uint32_t)blk >= a.num_blocks) {
-                if (c == 0) atomicOr(a.err, KV_DEVERR_BLOCK_RANGE);
-                continue;
-            }
-            uint8_t *to = base + (int64_t)blk * a.block_stride + (int64_t)(pos - page * a.block_size) * a.tok_stride;
-            float v[8];
-            if constexpr (MX4) {
-                const uint32_t e = 8 * j;
-                load4(v, from + e);
-                load4(v + 4, from + e + 4);
-                if (key) {
-                    float other[8] = {};
-                    if (!ADJACENT) {
-                        load4(other, from + partner(e, pairs));
-                        load4(other + 4, from + partner(e + 4, pairs));
-                    }
-                    turn_wide<ADJACENT>(v, other, e, pairs, cs64[u]);
-                }
-                const uint32_t s = mx4_scale_of(v);
-                *(uint32_t *)(to + e / 2) = to_mx4(v, s);
-                if (j % 4 == 0) to[a.dim / 2 + j / 4] = (uint8_t)s;
-            } else {
-                const Unit<ADJACENT> unit(j, key ? pairs : 0);
-                load4(v, from + unit.a);
-                load4(v + 4, from + unit.b);
-                if (unit.turns) turn_unit<ADJACENT>(v, &cs[u][4 * j]);
-                if (CACHE == kE4m3) {
-                    *(uint32_t *)(to + unit.a) = to_e4m3(v, scale);
-                    *(uint32_t *)(to + unit.b) = to_e4m3(v + 4, scale);
-                } else {
-                    store4((T *)to + unit.a, v);
-                    store4((T *)to + unit.b, v + 4);
-                }
-            }
-        }
+    for (int i = 0; i < N / 4; ++i) {
+        uint32_t w = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w |= (uint32_t)v[4 * i + k] << (8 * k);
+        const Vec<__bf16>::x4 y = from_e4m3<__bf16>(w);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[4 * i + k] = (float)y[k];
     }
 }
 
-template <class T, bool ADJACENT>
+// ---- append with a rotation on the way --------------------------------------------
+
+// A workgroup's tokens, of an item's: 2^lg_split workgroups to an item.
+struct Part {
+    int32_t item, begin;
+    int32_t count;  // below 1: none
+    __device__ __forceinline__ Part(const AttnLaunch &a, uint32_t lg_split, AppendItem *it)
+    {
+        item = (int32_t)(blockIdx.x >> lg_split);
+        begin = (int32_t)(blockIdx.x & ((1u << lg_split) - 1)) * (KVX_APPEND_TOKENS >> lg_split);
+        count = 0;
+        if (item >= plan_record(a.head).n_append) return;
+        *it = plan_record(a.append + item);
+        count = min(it->count - begin, KVX_APPEND_TOKENS >> lg_split);
+    }
+};
+// Layers to a workgroup: `most` where KVX_DEEP_GROUPS workgroups remain (four layers of 16 tokens read: 4.0 us with a layer
+// each, 4.8 with all), and no more than 65535 along y.
+inline int32_t layers_of(int64_t most, int64_t groups, int32_t layers)
+{
+    return (int32_t)std::max<int64_t>({1, std::min(most, groups * layers / KVX_DEEP_GROUPS), (layers + 65534) / 65535});
+}
+// Two tokens to a workgroup; all eight where a token's units are few (32 layers of 2860 tokens of 2 heads read: 12.9 us,
+// 11.7; of 8 heads, one layer: 10.8, 13.2).
+inline uint32_t lg_split(uint32_t units) { return units <= KVX_FEW_UNITS ? 0 : 2; }
+static_assert(KVX_APPEND_SPLIT == 4, "lg_split");
+
+// One new token's place in its region, from the region's row of head 0 on; its block id has been read.
+__device__ __forceinline__ int64_t place_of(const AttnLaunch &a, uint32_t pos, int32_t blk)
+{
+    return (int64_t)blk * a.block_stride + (int64_t)(pos - div_by(pos, a.bs_magic, a.bs_shift) * a.block_size) * a.tok_stride;
+}
+
+// A workgroup's units of a token: keys, values and queries, or, in mx4 pools, queries alone, in one sequence over all tokens.
+template <class T, int CACHE, bool ADJACENT, int VEC>
+struct AppendUnit {
+    uint32_t u, c, h, j, units;
+    bool there, key, query;
+    __device__ __forceinline__ AppendUnit(const AppendRotated &x, uint32_t i, uint32_t count, int64_t row0)
+    {
+        const AttnLaunch &a = x.attn;
+        units = (uint32_t)a.dim / (2 * VEC);
+        const uint32_t kv = CACHE == kMx4 ? 0 : units * (uint32_t)a.heads;
+        const uint32_t all = 2 * kv + (a.q ? units * (uint32_t)(a.heads * a.group) : 0);
+        u = div_by(i, x.all_magic, x.all_shift);
+        c = i - u * all;
+        there = i < count * all && row0 + u < a.n_tokens;
+        key = c < kv;
+        query = c >= 2 * kv;
+        const uint32_t hc = key ? c : query ? c - 2 * kv : c - kv;
+        h = div_by(hc, x.unit_magic, x.unit_shift);
+        j = hc - h * units;
+    }
+};
+// The same of an mx4 pool's keys and values: eight consecutive elements to a thread, a group to four of them.
+struct AppendEight {
+    uint32_t u, c, h, e;
+    bool there, key;
+    __device__ __forceinline__ AppendEight(const AppendRotated &x, uint32_t i, uint32_t count, int64_t row0)
+    {
+        const AttnLaunch &a = x.attn;
+        const uint32_t eights = (uint32_t)a.dim / 8, each = eights * (uint32_t)a.heads;
+        u = div_by(i, x.each_magic, x.each_shift);
+        c = i - u * 2 * each;
+        there = i < count * 2 * each && row0 + u < a.n_tokens;
+        key = c < each;
+        const uint32_t hc = key ? c : c - each;
+        h = div_by(hc, x.eight_magic, x.eight_shift);
+        e = 8 * (hc - h * eights);
+    }
+};
+
+// A workgroup works out the angles of its tokens once, for all heads, and then streams their units through, kAhead (of mx4
+// keys and values kAhead8) of them loaded by a thread before the first is turned.  An mx4 pool's keys and values, with angles
+// and sums of 64 bits, and the queries have workgroups of their own (blockIdx.y): the first loads of the former are on their
+// way while the angles are worked out.
+template <class T, int CACHE, bool ADJACENT, int VEC>
+__global__ __launch_bounds__(kThreads) void append_rotated(const AppendRotated x)
+{
+    typedef typename Run<T, VEC>::type TV;
+    typedef typename Vec<T>::x8 T8;
+    typedef typename Vec<T>::x4 T4;
+    typedef AppendUnit<T, CACHE, ADJACENT, VEC> At;
+    constexpr bool MX4 = CACHE == kMx4;
+    constexpr int kAhead = 3, kAhead8 = 2;
+    __shared__ float2 cs[KVX_APPEND_TOKENS][kMaxPairs];
+    __shared__ double2 cs64[MX4 ? KVX_APPEND_TOKENS : 1][MX4 ? kMaxPairs : 1];
+    const AttnLaunch &a = x.attn;
+    AppendItem it;
+    const Part part(a, x.lg_split, &it);
+    if (part.count < 1) return;
+    const uint32_t begin = part.begin, count = part.count, pairs = x.rot.pairs;
+    const int64_t row0 = (int64_t)it.row + begin;
+    const uint32_t pos0 = (uint32_t)it.pos + begin;
+    const uint32_t units = (uint32_t)a.dim / (2 * VEC);
+    const bool wide = MX4 && blockIdx.y == 0;
+    const uint32_t all = wide ? 0 : units * (uint32_t)a.heads * ((MX4 ? 0 : 2) + (a.q ? (uint32_t)a.group : 0));
+    const uint32_t eights = wide ? 2 * ((uint32_t)a.dim / 8) * (uint32_t)a.heads : 0;
+    auto row_of = [&](const auto &at, bool key, bool query) __attribute__((always_inline)) -> const T * {
+        const int64_t row = row0 + at.u;
+        return query ? (const T *)a.q + row * a.q_token + (int64_t)at.h * a.q_head
+               : key ? (const T *)a.k_new + row * a.k_token + (int64_t)at.h * a.k_head
+                     : (const T *)a.v_new + row * a.v_token + (int64_t)at.h * a.v_head;
+    };
+    auto block_of = [&](uint32_t u) __attribute__((always_inline)) { return it.table[div_by(pos0 + u, a.bs_magic, a.bs_shift)]; };
+
+    TV va[kAhead], vb[kAhead];
+    int32_t blk[kAhead];
+    auto ask = [&](uint32_t i0) __attribute__((always_inline)) {
+#pragma unroll
+        for (int m = 0; m < kAhead; ++m) {
+            const At at(x, i0 + m * kThreads, count, row0);
+            if (!at.there) continue;
+            const Unit<ADJACENT, VEC> unit(at.j, at.key || at.query ? pairs : 0);
+            const T *from = row_of(at, at.key, at.query);
+            va[m] = *(const TV *)(from + unit.a);
+            vb[m] = *(const TV *)(from + unit.b);
+            blk[m] = 0;
+            if (!at.query) blk[m] = block_of(at.u);
+        }
+    };
+    T8 v8[kAhead8];
+    T4 o4[kAhead8][2];
+    int32_t blk8[kAhead8];
+    auto ask8 = [&](uint32_t i0) __attribute__((always_inline)) {
+#pragma unroll
+        for (int m = 0; m < kAhead8; ++m) {
+            const AppendEight at(x, i0 + m * kThreads, count, row0);
+            if (!at.there) continue;
+            const T *from = row_of(at, at.key, false);
+            v8[m] = *(const T8 *)(from + at.e);
+            if (at.key && !ADJACENT) {
+                o4[m][0] = *(const T4 *)(from + partner(at.e, pairs));
+                o4[m][1] = *(const T4 *)(from + partner(at.e + 4, pairs));
+            }
+            blk8[m] = block_of(at.u);
+        }
+    };
+    if (wide) ask8(threadIdx.x);
+    for (uint32_t i = threadIdx.x; i < count * pairs; i += kThreads) {
+        const uint32_t u = div_by(i, x.pair_magic, x.pair_shift), pair = i - u * pairs;
+        if (row0 + u >= a.n_tokens) continue;
+        const int32_t pos = x.positions ? x.positions[row0 + u] : (int32_t)(pos0 + u);
+        const uint64_t t = turns_of(x.rot, pos, pair);
+        if (!wide) cs[u][pair] = turn32(t, x.rot.amplitude);
+        else if constexpr (MX4) cs64[u][pair] = turn64(t, x.rot.amplitude);
+    }
+    __syncthreads();
+
+    if constexpr (MX4) {
+        for (uint32_t i0 = threadIdx.x; i0 < count * eights;) {
+#pragma unroll
+            for (int m = 0; m < kAhead8; ++m) {
+                const AppendEight at(x, i0 + m * kThreads, count, row0);
+                if (!at.there) continue;
+                if ((uint32_t)blk8[m] >= a.num_blocks) {
+                    if (at.c == 0) atomicOr(a.err, KV_DEVERR_BLOCK_RANGE);
+                    continue;
+                }
+                float v[8], other[8] = {};
+                values_of<T, 8>(v, v8[m]);
+                if (at.key && !ADJACENT) {
+                    values_of<T, 4>(other, o4[m][0]);
+                    values_of<T, 4>(other + 4, o4[m][1]);
+                }
+                if (at.key) turn_wide<ADJACENT>(v, other, at.e, pairs, cs64[at.u]);
+                uint8_t *to = (at.key ? a.k_base : a.v_base) + place_of(a, pos0 + at.u, blk8[m]) + (int64_t)at.h * a.head_stride;
+                const uint32_t s = mx4_scale_of(v);
+                *(uint32_t *)(to + at.e / 2) = to_mx4(v, s);
+                if (at.e % 32 == 0) to[a.dim / 2 + at.e / 32] = (uint8_t)s;
+            }
+            i0 += kAhead8 * kThreads;
+            if (i0 < count * eights) ask8(i0);
+        }
+    }
+    if (wide) return;
+    ask(threadIdx.x);
+    for (uint32_t i0 = threadIdx.x; i0 < count * all;) {
+#pragma unroll
+        for (int m = 0; m < kAhead; ++m) {
+            const At at(x, i0 + m * kThreads, count, row0);
+            if (!at.there) continue;
+            const Unit<ADJACENT, VEC> unit(at.j, at.key || at.query ? pairs : 0);
+            float v[2 * VEC];
+            values_of<T, VEC>(v, va[m]);
+            values_of<T, VEC>(v + VEC, vb[m]);
+            if (unit.turns) turn_unit<ADJACENT, VEC>(v, &cs[at.u][VEC * at.j]);
+            if (at.query) {
+                T *to = (T *)a.out + (row0 + at.u) * a.out_token + (int64_t)at.h * a.out_head;
+                store_past(to + unit.a, run_of<T, VEC>(v));
+                store_past(to + unit.b, run_of<T, VEC>(v + VEC));
+                continue;
+            }
+            if ((uint32_t)blk[m] >= a.num_blocks) {
+                if (at.c == 0) atomicOr(a.err, KV_DEVERR_BLOCK_RANGE);
+                continue;
+            }
+            uint8_t *to = (at.key ? a.k_base : a.v_base) + place_of(a, pos0 + at.u, blk[m]) + (int64_t)at.h * a.head_stride;
+            if constexpr (CACHE == kE4m3) {
+                const float scale = at.key ? a.k_scale : a.v_scale;
+                store_past(to + unit.a, to_e4m3<VEC>(v, scale));
+                store_past(to + unit.b, to_e4m3<VEC>(v + VEC, scale));
+            } else {
+                store_past((T *)to + unit.a, run_of<T, VEC>(v));
+                store_past((T *)to + unit.b, run_of<T, VEC>(v + VEC));
+            }
+        }
+        i0 += kAhead * kThreads;
+        if (i0 < count * all) ask(i0);
+    }
+}
+
+template <class T, bool ADJACENT, int VEC>
 const void *append_kernel(int kv_type)
 {
     switch (cache_of(kv_type)) {
-    case kMx4: return (const void *)&append_rotated<T, kMx4, ADJACENT>;
-    case kE4m3: return (const void *)&append_rotated<T, kE4m3, ADJACENT>;
-    default: return (const void *)&append_rotated<T, kHalves, ADJACENT>;
+    case kMx4: return (const void *)&append_rotated<T, kMx4, ADJACENT, VEC>;
+    case kE4m3: return (const void *)&append_rotated<T, kE4m3, ADJACENT, VEC>;
+    default: return (const void *)&append_rotated<T, kHalves, ADJACENT, VEC>;
     }
+}
+template <class T>
+const void *append_kernel(int kv_type, bool adjacent, int vec)
+{
+    return adjacent ? (vec == 8 ? append_kernel<T, true, 8>(kv_type) : append_kernel<T, true, 4>(kv_type))
+                    : (vec == 8 ? append_kernel<T, false, 8>(kv_type) : append_kernel<T, false, 4>(kv_type));
 }
 
 int launch_append_rotated(const AppendRotated &a, int q_type, int kv_type, uint32_t grid, hipStream_t stream)
 {
     AppendRotated arg = a;
-    set_div((uint32_t)a.attn.dim / 8, &arg.unit_magic, &arg.unit_shift);
+    const AttnLaunch &l = a.attn;
+    const int vec = unit_vec(a.rot.pairs, l.dim);
+    const bool mx4 = kv_type == KV_TYPE_MX4;
+    const uint32_t units = (uint32_t)l.dim / (2 * vec), eights = (uint32_t)l.dim / 8;
+    const uint32_t all = units * (uint32_t)l.heads * ((mx4 ? 0 : 2) + (l.q ? (uint32_t)l.group : 0));
+    const uint32_t threads = std::max(all, mx4 ? 2 * eights * (uint32_t)l.heads : 0);
+    // Angles of 64 bits, and 17 bytes written for 64 read: eight tokens to a workgroup where there are many (7874 tokens of 32
+    // heads on 8: 36.4 -> 31.1 us; of 16-bit pools 33.6 -> 35.4, e4m3 20.9 -> 24.0).
+    arg.lg_split = mx4 && 2 * grid >= KVX_DEEP_GROUPS ? 0 : lg_split(threads);
+    set_div(units, &arg.unit_magic, &arg.unit_shift);
+    set_div(all ? all : 1, &arg.all_magic, &arg.all_shift);
+    set_div(a.rot.pairs ? a.rot.pairs : 1, &arg.pair_magic, &arg.pair_shift);
+    set_div(eights, &arg.eight_magic, &arg.eight_shift);
+    set_div(2 * eights * (uint32_t)l.heads, &arg.each_magic, &arg.each_shift);
     void *args[] = {&arg};
-    const uint32_t all = (uint32_t)a.attn.dim / 8 * (uint32_t)a.attn.heads * (2 + (a.attn.q ? (uint32_t)a.attn.group : 0));
-    const uint32_t slices = std::min((all + kThreads - 1) / kThreads, 65535u);
-    const void *fn = q_type == KV_TYPE_F16
-                         ? (a.rot.adjacent ? append_kernel<_Float16, true>(kv_type) : append_kernel<_Float16, false>(kv_type))
-                         : (a.rot.adjacent ? append_kernel<__bf16, true>(kv_type) : append_kernel<__bf16, false>(kv_type));
-    return (int)hipLaunchKernel(fn, dim3(grid * KVX_APPEND_SPLIT, slices), dim3(kThreads), args, 0, stream);
+    const void *fn = q_type == KV_TYPE_F16 ? append_kernel<_Float16>(kv_type, a.rot.adjacent != 0, vec)
+                                           : append_kernel<__bf16>(kv_type, a.rot.adjacent != 0, vec);
+    return (int)hipLaunchKernel(fn, dim3(grid << arg.lg_split, mx4 && l.q ? 2 : 1), dim3(kThreads), args, 0, stream);
 }
 
 // Appends to mx4 pools without a rotation: the same kernel with no pairs and no queries.
@@ -327,55 +486,68 @@ int launch_append_mx4(const AttnLaunch &a, int q_type, uint32_t grid, hipStream_
 
 // ---- cached tokens as 16-bit rows ---------------------------------------------------
 
-// The append's items the other way; layers along y.  A thread owns one unit of both tokens' keys, then values.
+// The append's items the other way.  Eight elements to a thread; a unit's places are worked out once for all layers of
+// a workgroup, and kAhead loads asked for before the first is written.
 template <class T, int CACHE>
 __global__ __launch_bounds__(kThreads) void read_tokens(const ReadLaunch x)
 {
     typedef typename Vec<T>::x8 T8;
     typedef typename Vec<T>::x4 T4;
-    constexpr int kBatch = KVX_APPEND_TOKENS / KVX_APPEND_SPLIT;
+    typedef typename std::conditional<CACHE == kMx4, uint32_t, typename std::conditional<CACHE == kE4m3, uint2, T8>::type>::type Held;
+    constexpr int kAhead = 4;
     const AttnLaunch &a = x.attn;
-    const AppendItem it = plan_record(a.append + blockIdx.x / KVX_APPEND_SPLIT);
-    if ((int32_t)(blockIdx.x / KVX_APPEND_SPLIT) >= plan_record(a.head).n_append) return;
-    const uint32_t begin = blockIdx.x % KVX_APPEND_SPLIT * kBatch;
-    const uint32_t end = min((uint32_t)it.count, begin + kBatch);
-    const uint32_t units = (uint32_t)a.dim / 8, kv = units * (uint32_t)a.heads;
-    for (int32_t layer = blockIdx.y; layer < x.layers; layer += gridDim.y) {
-        for (uint32_t c = threadIdx.x; c < 2 * kv; c += kThreads) {
-            const bool key = c < kv;
-            if (!(key ? x.k : x.v)) continue;
-            const uint32_t hc = key ? c : c - kv, h = div_by(hc, x.unit_magic, x.unit_shift), j = hc - h * units;
-            const uint8_t *base = ((uint8_t *const KVX_CONST *)x.regions)[2 * layer + (key ? 0 : 1)] + (int64_t)h * a.head_stride;
-            T *out = key ? (T *)x.k + layer * x.k_layer + (int64_t)h * a.k_head : (T *)x.v + layer * x.v_layer + (int64_t)h * a.v_head;
-            const int64_t out_tok = key ? a.k_token : a.v_token;
-            const float scale = key ? a.k_scale : a.v_scale;
+    AppendItem it;
+    const Part part(a, x.lg_split, &it);
+    if (part.count < 1) return;
+    const uint32_t begin = part.begin, count = part.count;
+    const uint32_t units = (uint32_t)a.dim / 8, kv = units * (uint32_t)a.heads, all = x.k && x.v ? 2 * kv : kv;
+    const int32_t layer0 = (int32_t)blockIdx.y * x.deep, layer1 = min(layer0 + x.deep, x.layers);
+    for (uint32_t i = threadIdx.x; i < count * all; i += kThreads) {
+        const uint32_t u = div_by(i, x.all_magic, x.all_shift), c = i - u * all;
+        const int64_t row = (int64_t)it.row + begin + u;
+        if (row >= a.n_tokens) continue;
+        const bool key = x.k && c < kv;
+        const uint32_t hc = c < kv ? c : c - kv, h = div_by(hc, x.unit_magic, x.unit_shift), j = hc - h * units;
+        const uint32_t pos = (uint32_t)it.pos + begin + u;
+        const int32_t blk = it.table[div_by(pos, a.bs_magic, a.bs_shift)];
+        if ((uint32_t)blk >= a.num_blocks) {
+            if (c == 0) atomicOr(a.err, KV_DEVERR_BLOCK_RANGE);
+            continue;
+        }
+        const int64_t off = place_of(a, pos, blk) + (int64_t)h * a.head_stride;
+        T *to = key ? (T *)x.k + layer0 * x.k_layer + row * a.k_token + (int64_t)h * a.k_head + 8 * j
+                    : (T *)x.v + layer0 * x.v_layer + row * a.v_token + (int64_t)h * a.v_head + 8 * j;
+        const int64_t layer_step = key ? x.k_layer : x.v_layer;
+        for (int32_t layer = layer0; layer < layer1; layer += kAhead) {
+            uint8_t *const KVX_CONST *regions = (uint8_t *const KVX_CONST *)x.regions + 2 * (int64_t)layer;
+            Held held[kAhead];
+            uint32_t scale[kAhead];
 #pragma unroll
-            for (uint32_t u = 0; u < kBatch; ++u) {
-                const uint32_t t = begin + u;
-                const int64_t row = (int64_t)it.row + t;
-                if (t >= end || row >= a.n_tokens) continue;
-                const uint32_t pos = (uint32_t)it.pos + t, page = div_by(pos, a.bs_magic, a.bs_shift);
-                const int32_t blk = it.table[page];
-                if ((uint32_t)blk >= a.num_blocks) {
-                    atomicOr(a.err, KV_DEVERR_BLOCK_RANGE);
-                    continue;
-                }
-                const uint8_t *from = base + (int64_t)blk * a.block_stride + (int64_t)(pos - page * a.block_size) * a.tok_stride;
+            for (int m = 0; m < kAhead; ++m) {
+                if (layer + m >= layer1) break;
+                const uint8_t *from = (key ? regions[2 * m] : regions[2 * m + 1]) + off;
+                held[m] = *(const Held *)(from + j * sizeof(Held));
+                if constexpr (CACHE == kMx4) scale[m] = from[a.dim / 2 + j / 4];
+            }
+#pragma unroll
+            for (int m = 0; m < kAhead; ++m) {
+                if (layer + m >= layer1) break;
                 T8 v;
                 if constexpr (CACHE == kMx4) {
-                    v = from_mx4<T>(*(const uint32_t *)(from + 4 * j), mx4_scale(from[a.dim / 2 + j / 4]));
+                    v = from_mx4<T>(held[m], mx4_scale(scale[m]));
                 } else if constexpr (CACHE == kE4m3) {
-                    const uint2 w = *(const uint2 *)(from + 8 * j);
-                    const T4 lo = from_e4m3<T>(w.x), hi = from_e4m3<T>(w.y);
+                    const T4 lo = from_e4m3<T>(held[m].x), hi = from_e4m3<T>(held[m].y);
+                    const float by = key ? a.k_scale : a.v_scale;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        v[i] = (T)((float)lo[i] * scale);
-                        v[4 + i] = (T)((float)hi[i] * scale);
+                    for (int k = 0; k < 4; ++k) {
+                        v[k] = (T)((float)lo[k] * by);
+                        v[4 + k] = (T)((float)hi[k] * by);
                     }
                 } else {
-                    v = *(const T8 *)(from + 16 * j);
+                    v = held[m];
                 }
-                *(T8 *)(out + row * out_tok + 8 * j) = v;
+                store_past(to, v);
+                to += layer_step;
             }
         }
     }
@@ -384,7 +556,10 @@ __global__ __launch_bounds__(kThreads) void read_tokens(const ReadLaunch x)
 int launch_read(const ReadLaunch &a, int q_type, int kv_type, uint32_t grid, hipStream_t stream)
 {
     ReadLaunch arg = a;
-    set_div((uint32_t)a.attn.dim / 8, &arg.unit_magic, &arg.unit_shift);
+    const uint32_t units = (uint32_t)a.attn.dim / 8, all = units * (uint32_t)a.attn.heads * (a.k && a.v ? 2 : 1);
+    arg.lg_split = lg_split(all);
+    set_div(units, &arg.unit_magic, &arg.unit_shift);
+    set_div(all, &arg.all_magic, &arg.all_shift);
     void *args[] = {&arg};
     const Cache cache = cache_of(kv_type);
     const void *fn = q_type == KV_TYPE_F16 ? (cache == kMx4    ? (const void *)&read_tokens<_Float16, kMx4>
@@ -393,25 +568,27 @@ int launch_read(const ReadLaunch &a, int q_type, int kv_type, uint32_t grid, hip
                                            : (cache == kMx4    ? (const void *)&read_tokens<__bf16, kMx4>
                                               : cache == kE4m3 ? (const void *)&read_tokens<__bf16, kE4m3>
                                                                : (const void *)&read_tokens<__bf16, kHalves>);
-    const uint32_t layers = (uint32_t)std::min(a.layers, 65535);
-    return (int)hipLaunchKernel(fn, dim3(grid * KVX_APPEND_SPLIT, layers), dim3(kThreads), args, 0, stream);
+    arg.deep = layers_of(KVX_READ_DEEP, (int64_t)grid << arg.lg_split, a.layers);
+    return (int)hipLaunchKernel(fn, dim3(grid << arg.lg_split, (a.layers + arg.deep - 1) / arg.deep), dim3(kThreads), args, 0, stream);
 }
 
 // ---- cached keys to other positions ---------------------------------------------------
 
 // An item is up to 16 tokens of one record, in one layer (y).  All of a record's tokens turn by the same angles, so a
 // workgroup works them out once, with the places of its tokens, and then streams the rows through.
-template <class T, int CACHE, bool ADJACENT>
+template <class T, int CACHE, bool ADJACENT, int VEC>
 __global__ __launch_bounds__(kThreads) void shift_keys(const ShiftLaunch x)
 {
     constexpr bool MX4 = CACHE == kMx4;
     __shared__ float2 cs[MX4 ? 1 : kMaxPairs];
     __shared__ double2 cs64[MX4 ? kMaxPairs : 1];
     __shared__ int64_t place[KVX_SHIFT_TOKENS];  // of each token, or -1
+    constexpr int kRows = MX4 ? 2 : 4, kLayers = MX4 ? 2 : 1;
     const KVX_CONST ShiftRec *recs =
         x.recs ? (const KVX_CONST ShiftRec *)x.recs
                : (const KVX_CONST ShiftRec *)((const KVX_CONST uint8_t *)__builtin_amdgcn_kernarg_segment_ptr() + offsetof(ShiftLaunch, inl));
-    const uint32_t pairs = x.rot.pairs, units = (uint32_t)x.dim / 8;
+    const uint32_t pairs = x.rot.pairs;
+    const int32_t layer0 = (int32_t)blockIdx.y * x.deep;
     for (int32_t item = blockIdx.x; item < x.items; item += gridDim.x) {
         int32_t r = 0, n = x.n;  // the last record that begins at or before the item
         while (n > 1) {
@@ -442,67 +619,111 @@ __global__ __launch_bounds__(kThreads) void shift_keys(const ShiftLaunch x)
             place[t] = at;
         }
         __syncthreads();
-        for (int32_t layer = blockIdx.y; layer < x.layers; layer += gridDim.y) {
-            uint8_t *base = ((uint8_t *const KVX_CONST *)x.regions)[2 * layer];
-            // rows of the item in the order in which they lie: token, head, or head, token
-            auto row_of = [&](uint32_t r) __attribute__((always_inline)) -> uint8_t * {
-                const bool by_token = x.tok_stride > x.head_stride;
-                const uint32_t t = by_token ? div_by(r, x.head_magic, x.head_shift) : r % KVX_SHIFT_TOKENS;
-                const uint32_t h = by_token ? r - t * (uint32_t)x.heads : r / KVX_SHIFT_TOKENS;
-                const int64_t at = place[t];
-                return at < 0 ? nullptr : base + at + (int64_t)h * x.head_stride;
-            };
-            const uint32_t rows = KVX_SHIFT_TOKENS * (uint32_t)x.heads;
-            if constexpr (MX4) {
-                // A row's units lie in one wave: all of them have been read before the first is written, as the wave waits for
-                // its loads as one.
-                const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-                const uint32_t slot = div_by(lane, x.unit_magic, x.unit_shift), j = lane - slot * units, each = 64 / units;
-                for (uint32_t r0 = wave * each; r0 < rows; r0 += kWaves * each) {
-                    uint8_t *row = slot < each && r0 + slot < rows ? row_of(r0 + slot) : nullptr;
-                    if (!row) continue;
-                    const uint32_t e = 8 * j;
-                    const Vec<float>::x8 w = from_mx4<float>(*(const uint32_t *)(row + e / 2), mx4_scale(row[x.dim / 2 + e / 32]));
-                    float v[8], other[8] = {};
+        // A thread keeps its place in a row, and with it its angles; kRows rows and kLayers layers are loaded before the first
+        // is turned.  Rows follow each other as they lie: (token, head), or (head, token) in pages by heads.
+        const uint32_t rows = KVX_SHIFT_TOKENS * (uint32_t)x.heads;
+        const bool by_token = x.tok_stride > x.head_stride;
+        const uint32_t units = MX4 ? (uint32_t)x.dim / 8 : pairs / VEC, span = MX4 ? 64 : kThreads;
+        const uint32_t lane = threadIdx.x % span, slot = div_by(lane, x.unit_magic, x.unit_shift), j = lane - slot * units;
+        const uint32_t each = span / units, step = each * (kThreads / span), slot0 = slot + threadIdx.x / span * each;
+        const int32_t layer1 = min(layer0 + x.deep, x.layers);
+        // of an mx4 row the unit's sums, else its turns
+        double c[MX4 ? 8 : 1], sn[MX4 ? 8 : 1];
+        float2 turn[MX4 ? 1 : VEC];
+        const uint32_t e = 8 * j, p0 = partner(e, pairs), p1 = partner(e + 4, pairs);
+        const int lane0 = (int)(lane - j + p0 / 8), lane1 = (int)(lane - j + p1 / 8);
+        if constexpr (MX4) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = w[i];
-                    if (!ADJACENT) {
-                        const uint32_t p0 = partner(e, pairs), p1 = partner(e + 4, pairs);
-                        const Vec<float>::x8 lo = from_mx4<float>(*(const uint16_t *)(row + p0 / 2), mx4_scale(row[x.dim / 2 + p0 / 32]));
-                        const Vec<float>::x8 hi = from_mx4<float>(*(const uint16_t *)(row + p1 / 2), mx4_scale(row[x.dim / 2 + p1 / 32]));
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t at = e + i, pair = ADJACENT ? at / 2 : at < pairs ? at : at - pairs;
+                const bool turns = at < 2 * pairs, first = ADJACENT ? i % 2 == 0 : at < pairs;
+                const double2 t = cs64[turns ? pair : 0];
+                c[i] = turns ? t.x : 1.;
+                sn[i] = !turns ? 0. : first ? -t.y : t.y;
+            }
+        } else {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) other[i] = lo[i], other[4 + i] = hi[i];
+            for (int i = 0; i < VEC; ++i) turn[i] = cs[VEC * j + i];
+        }
+        for (uint32_t r0 = 0; r0 < rows; r0 += kRows * step) {
+            int64_t off[kRows];
+#pragma unroll
+            for (int k = 0; k < kRows; ++k) {
+                const uint32_t r = r0 + k * step + slot0, q = by_token ? div_by(r, x.head_magic, x.head_shift) : r / KVX_SHIFT_TOKENS;
+                const uint32_t t = by_token ? q : r % KVX_SHIFT_TOKENS, h = by_token ? r - q * (uint32_t)x.heads : q;
+                off[k] = slot < each && r < rows ? place[t] : -1;
+                if (off[k] >= 0) off[k] += (int64_t)h * x.head_stride;
+            }
+            for (int32_t layer = layer0; layer < layer1; layer += kLayers) {
+                uint8_t *const KVX_CONST *regions = (uint8_t *const KVX_CONST *)x.regions + 2 * (int64_t)layer;
+                if constexpr (MX4) {
+                    uint32_t w[kRows * kLayers], scale[kRows * kLayers];
+#pragma unroll
+                    for (int m = 0; m < kRows * kLayers; ++m) {
+                        w[m] = scale[m] = 0;
+                        if (off[m % kRows] < 0 || layer + m / kRows >= layer1) continue;
+                        const uint8_t *row = regions[2 * (m / kRows)] + off[m % kRows];
+                        w[m] = *(const uint32_t *)(row + e / 2);
+                        scale[m] = row[x.dim / 2 + e / 32];
                     }
-                    turn_wide<ADJACENT>(v, other, e, pairs, cs64);
-                    const uint32_t s = mx4_scale_of(v);
-                    *(uint32_t *)(row + e / 2) = to_mx4(v, s);
-                    if (j % 4 == 0) row[x.dim / 2 + j / 4] = (uint8_t)s;
-                }
-            } else {
-                // only the units that turn
-                const uint32_t each = pairs / 4;
-                for (uint32_t i = threadIdx.x; i < rows * each; i += kThreads) {
-                    const uint32_t r = div_by(i, x.unit_magic, x.unit_shift), j = i - r * each;
-                    uint8_t *row = row_of(r);
-                    if (!row) continue;
-                    const Unit<ADJACENT> unit(j, pairs);
-                    float v[8];
-                    if constexpr (CACHE == kE4m3) {
-                        const Vec<__bf16>::x4 lo = from_e4m3<__bf16>(*(const uint32_t *)(row + unit.a));
-                        const Vec<__bf16>::x4 hi = from_e4m3<__bf16>(*(const uint32_t *)(row + unit.b));
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) v[k] = (float)lo[k], v[4 + k] = (float)hi[k];
-                    } else {
-                        load4(v, (const T *)row + unit.a);
-                        load4(v + 4, (const T *)row + unit.b);
+                    for (int m = 0; m < kRows * kLayers; ++m) {
+                        if (layer + m / kRows >= layer1) continue;
+                        // A row's units lie in one wave, so a unit's partners come from the lanes that hold them.
+                        Vec<float>::x8 v = from_mx4<float>(w[m], mx4_scale(scale[m])), other;
+                        if (ADJACENT) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) other[i] = e < 2 * pairs ? v[i ^ 1] : v[i];  // times 0 of its own sign
+                        } else {
+                            const uint32_t w0 = __shfl(w[m], lane0), w1 = __shfl(w[m], lane1);
+                            const uint32_t s0 = __shfl(scale[m], lane0), s1 = __shfl(scale[m], lane1);
+                            const Vec<float>::x8 lo = from_mx4<float>(p0 % 8 ? w0 >> 16 : w0, mx4_scale(s0));
+                            const Vec<float>::x8 hi = from_mx4<float>(p1 % 8 ? w1 >> 16 : w1, mx4_scale(s1));
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) other[i] = lo[i], other[4 + i] = hi[i];
+                        }
+                        if (off[m % kRows] < 0) continue;
+                        float y[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) y[i] = to_odd(__builtin_fma((double)v[i], c[i], (double)other[i] * sn[i]));
+                        uint8_t *row = regions[2 * (m / kRows)] + off[m % kRows];
+                        const uint32_t s = mx4_scale_of(y);
+                        *(uint32_t *)(row + e / 2) = to_mx4(y, s);
+                        if (j % 4 == 0) row[x.dim / 2 + j / 4] = (uint8_t)s;
                     }
-                    turn_unit<ADJACENT>(v, &cs[4 * j]);
-                    if constexpr (CACHE == kE4m3) {
-                        *(uint32_t *)(row + unit.a) = to_e4m3(v, 1.f);
-                        *(uint32_t *)(row + unit.b) = to_e4m3(v + 4, 1.f);
-                    } else {
-                        store4((T *)row + unit.a, v);
-                        store4((T *)row + unit.b, v + 4);
+                } else {
+                    // only the units that turn
+                    typedef typename std::conditional<CACHE == kE4m3, uint8_t, T>::type E;
+                    typedef typename Run<E, VEC>::type EV;
+                    const Unit<ADJACENT, VEC> unit(j, pairs);
+                    EV va[kRows], vb[kRows];
+#pragma unroll
+                    for (int k = 0; k < kRows; ++k) {
+                        if (off[k] < 0) continue;
+                        const E *row = (const E *)(regions[0] + off[k]);
+                        va[k] = *(const EV *)(row + unit.a);
+                        vb[k] = *(const EV *)(row + unit.b);
+                    }
+#pragma unroll
+                    for (int k = 0; k < kRows; ++k) {
+                        if (off[k] < 0) continue;
+                        E *row = (E *)(regions[0] + off[k]);
+                        float v[2 * VEC];
+                        if constexpr (CACHE == kE4m3) {
+                            values_of_e4m3<VEC>(v, va[k]);
+                            values_of_e4m3<VEC>(v + VEC, vb[k]);
+                        } else {
+                            values_of<T, VEC>(v, va[k]);
+                            values_of<T, VEC>(v + VEC, vb[k]);
+                        }
+                        turn_unit<ADJACENT, VEC>(v, turn);
+                        if constexpr (CACHE == kE4m3) {
+                            *(EV *)(row + unit.a) = to_e4m3<VEC>(v, 1.f);
+                            *(EV *)(row + unit.b) = to_e4m3<VEC>(v + VEC, 1.f);
+                        } else {
+                            *(EV *)(row + unit.a) = run_of<T, VEC>(v);
+                            *(EV *)(row + unit.b) = run_of<T, VEC>(v + VEC);
+                        }
                     }
                 }
             }
@@ -511,28 +732,33 @@ __global__ __launch_bounds__(kThreads) void shift_keys(const ShiftLaunch x)
     }
 }
 
-template <bool ADJACENT>
+template <bool ADJACENT, int VEC>
 const void *shift_kernel(int kv_type)
 {
     switch (kv_type) {
-    case KV_TYPE_MX4: return (const void *)&shift_keys<__bf16, kMx4, ADJACENT>;
-    case KV_TYPE_E4M3: return (const void *)&shift_keys<__bf16, kE4m3, ADJACENT>;
-    case KV_TYPE_F16: return (const void *)&shift_keys<_Float16, kHalves, ADJACENT>;
-    default: return (const void *)&shift_keys<__bf16, kHalves, ADJACENT>;
+    case KV_TYPE_MX4: return (const void *)&shift_keys<__bf16, kMx4, ADJACENT, 4>;
+    case KV_TYPE_E4M3: return (const void *)&shift_keys<__bf16, kE4m3, ADJACENT, VEC>;
+    case KV_TYPE_F16: return (const void *)&shift_keys<_Float16, kHalves, ADJACENT, VEC>;
+    default: return (const void *)&shift_keys<__bf16, kHalves, ADJACENT, VEC>;
     }
 }
 
 int launch_shift(const ShiftLaunch &a, int kv_type, hipStream_t stream)
 {
     ShiftLaunch arg = a;
+    const int vec = unit_vec(a.rot.pairs, a.dim);
     // mx4 rows go by all their units, others by those that turn
-    set_div(kv_type == KV_TYPE_MX4 ? (uint32_t)a.dim / 8 : a.rot.pairs / 4, &arg.unit_magic, &arg.unit_shift);
+    const uint32_t units = kv_type == KV_TYPE_MX4 ? (uint32_t)a.dim / 8 : a.rot.pairs / vec;
+    set_div(units, &arg.unit_magic, &arg.unit_shift);
     set_div((uint32_t)a.heads, &arg.head_magic, &arg.head_shift);
     void *args[] = {&arg};
     const uint32_t items = (uint32_t)std::min(a.items, 1 << 20);
-    const uint32_t layers = (uint32_t)std::min(a.layers, 65535);
-    return (int)hipLaunchKernel(a.rot.adjacent ? shift_kernel<true>(kv_type) : shift_kernel<false>(kv_type), dim3(items, layers),
-                                dim3(kThreads), args, 0, stream);
+    const int64_t own = ((int64_t)KVX_SHIFT_TOKENS * a.heads * units + kThreads - 1) / kThreads;
+    arg.deep = layers_of(KVX_SHIFT_UNITS / own, a.items, a.layers);
+    const uint32_t layers = (uint32_t)((a.layers + arg.deep - 1) / arg.deep);
+    const void *fn = a.rot.adjacent ? (vec == 8 ? shift_kernel<true, 8>(kv_type) : shift_kernel<true, 4>(kv_type))
+                                    : (vec == 8 ? shift_kernel<false, 8>(kv_type) : shift_kernel<false, 4>(kv_type));
+    return (int)hipLaunchKernel(fn, dim3(items, layers), dim3(kThreads), args, 0, stream);
 }
 
 }  // namespace kvx
