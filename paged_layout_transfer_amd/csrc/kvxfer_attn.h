@@ -1079,7 +1079,7 @@ __global__ __launch_bounds__(256) void join(const AttnLaunch a)
 
 // The same for 4-bit pools, whose long contexts have as many parts as other pools' but took a quarter of the time: where
 // there are more than KVX_JOIN_MANY, a record holds one row and all of a workgroup's threads take it.  256 parts of 32 rows: 6.5
-// us, 16 to 22 with four rows to a workgroup.
+// us, 16 to 22 with four rows to a workgroup; up to 31 parts (16 sequences of a decode step) 4.7 either way.
 template <class T, int DP>
 __global__ __launch_bounds__(256) void join_mx4(const AttnLaunch a)
 {

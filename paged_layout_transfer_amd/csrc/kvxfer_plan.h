@@ -112,7 +112,7 @@ struct SplitCost {
 };
 // Measured in tiles of 128-wide 16-bit heads without a cap, and used for all: a 64-wide tile costs less, a capped
 // one more, and with them the costs in tiles.
-constexpr SplitCost kCostFew{2, 2, 10, 2}, kCostFewMx4{2, 2, 10, 2}, kCostMany{1, 4, 4, 8}, kCostHalf{1, 4, 5, 8};
+constexpr SplitCost kCostFew{2, 2, 10, 2}, kCostMany{1, 4, 4, 8}, kCostHalf{1, 4, 5, 8};
 // A tile with waves 0 to 3 at work takes 72 hundredths of the time of one with all (1.5 and
 // 2.1 us, 128-wide heads; 512 new tokens on 16 K cached, cut to one round either way: 217 and 155 us).
 constexpr int64_t kHalfTile = 72;
@@ -341,7 +341,7 @@ inline void build_plan(Plan &p, const PlanLimits &l, const kv_seq *seqs, int32_t
             packs.token_major = false;
             if (same)
                 p.whole.erase(std::remove_if(p.whole.begin(), p.whole.end(), [](const AttnItem &it) { return it.head; }), p.whole.end());
-            const Split split = choose_split(p, packs, l.slots_few, kCostFewMx4, true);
+            const Split split = choose_split(p, packs, l.slots_few, kCostFew, true);
             if (same) (void)pieces_of(p, l, seqs, n, true, KVX_ROWS_FEW, std::max<int64_t>(1, most));
             cut_packs(p, l, split, &prow);
         } else {
