@@ -537,7 +537,8 @@ KV_API int kv_mx4_row_bytes(int32_t head_dim, int32_t num_heads, int32_t *out);
  * chip, and the workspace of partial results (up to 200 MiB); it is set once a step and used
  * by every layer.  The pool has num_kv 2, elem_bytes 1 for KV_TYPE_E4M3 and KV_TYPE_MX4 and 2 else, head_dim <=
  * KV_MAX_ATTN_DIM, and num_q_heads * max_tokens < 2^31 (else KV_ERR_ARG), and head_dim *
- * elem_bytes a multiple of 16, of 4 for KV_TYPE_MX4 (KV_ERR_ALIGN).  create allocates all device memory the plan
+ * elem_bytes a multiple of 16, of 4 for KV_TYPE_MX4 (KV_ERR_ALIGN); a KV_TYPE_MX4 token has at most 2^27 elements,
+ * keys and values together (KV_ERR_ARG).  create allocates all device memory the plan
  * will use, on the current device, which is then the pool's, and waits for the device; it must
  * not be made while a stream captures (KV_ERR_HIP).  destroy waits for the device to be idle
  * first (KV_ERR_HIP, and the plan stays, while a stream captures, as for kv_pool_destroy); NULL is accepted.  A plan is destroyed before its pool, and graphs that hold its calls do not
@@ -610,7 +611,8 @@ KV_API int kv_rotation_destroy(kv_rotation *rotation);
  * token's position, of either sign; NULL takes its place in the cache.  Rows of no sequence are neither read
  * nor written.  q_out may be q with its strides; otherwise it overlaps nothing that the call reads.
  * Errors and capture as kv_append_tokens; also KV_ERR_ARG for a rotation wider than head_dim or of another
- * device, and rows of q_out that overlap.  A bad block id skips the token's k and v, not its q. */
+ * device, rows of q_out that overlap, and a token's q, k and v of more than 2^27 elements.  A bad block id skips the
+ * token's k and v, not its q. */
 KV_API int kv_append_rotated(kv_attn_plan *plan, int32_t layer, const kv_rotation *rotation, const kv_rotate_args *rotate,
                              const kv_append_args *args, hipStream_t stream);
 
@@ -618,21 +620,24 @@ KV_API int kv_append_rotated(kv_attn_plan *plan, int32_t layer, const kv_rotatio
  * q_type rows: 16-bit pools' rows as they are, k_scale or v_scale times an e4m3 element, KV_TYPE_MX4 rows' values, each
  * rounded once.  A plan whose sequences have q_len = kv_len reads caches whole.  Rows of no sequence, and of tokens
  * whose block id is out of range (reported), are left as they were.  One launch.  Errors and capture as
- * kv_append_tokens; also KV_ERR_ARG for an empty layer range, no array at all, and rows of an array that overlap. */
+ * kv_append_tokens; also KV_ERR_ARG for an empty layer range, no array at all, rows of an array that
+ * overlap, and a token's k and v of more than 2^27 elements. */
 KV_API int kv_read_tokens(kv_attn_plan *plan, int32_t layer_begin, int32_t layer_end, const kv_read_args *args,
                           hipStream_t stream);
 
-/* Moves cached keys to other positions: in layers [layer_begin, layer_end) the keys of each record's tokens turn
- * by delta positions, in place, without amplitude, and are rounded to the pool's type again; values stay.  For
- * tokens that were appended rotated and whose places change: the middle of a conversation is dropped and the rest
- * moves up, or a reloaded chunk is used behind another prefix.  kv_type is the pool's element type, the pool as
- * for kv_attn_plan_create.  An e4m3 element saturates at +-448; its scale does not matter.  No page position may
- * be named twice, and pages that others share turn for them too (kv_pool_fork_blocks, kv_copy_pages).  A block
- * id out of range is skipped and reported.  shifts is a host array of n (0 .. KV_MAX_SHIFTS) records, the tables are read
- * when the call runs.  One launch.  Errors: KV_ERR_ARG, KV_ERR_ALIGN, KV_ERR_RANGE as for kv_attn_plan_create and
- * kv_attn_plan_set, KV_ERR_ARG for a rotation wider than head_dim or of another device.  Under capture a call of
- * at most 64 records that are not empty is captured as its kernel once the pool has made a call outside the
- * capture; any other is refused with KV_ERR_CAPTURE. */
+/* Moves cached keys to other positions: in layers [layer_begin, layer_end) the keys of each record's tokens
+ * turn by delta positions, in place, without amplitude, and are rounded to the pool's type again; values
+ * stay. For tokens that were appended rotated and whose places change: the middle of a conversation is
+ * dropped and the rest moves up, or a reloaded chunk is used behind another prefix. kv_type is the pool's
+ * element type, the pool as for kv_attn_plan_create. An e4m3 element saturates at +-448; its scale does not
+ * matter. No page position may be named twice (KV_ERR_DUP for records of one table that overlap; tables
+ * that share pages are not looked into), and pages that others share turn for them too
+ * (kv_pool_fork_blocks, kv_copy_pages). A block id out of range is skipped and reported. shifts is a host
+ * array of n (0 .. KV_MAX_SHIFTS) records, the tables are read when the call runs. One launch. Errors:
+ * KV_ERR_ARG, KV_ERR_ALIGN, KV_ERR_RANGE as for kv_attn_plan_create and kv_attn_plan_set, KV_ERR_ARG for a
+ * rotation wider than head_dim or of another device, and a token's k and v of more than 2^27 elements.
+ * Under capture a call of at most 64 records that are not empty is captured as its kernel once the pool has
+ * made a call outside the capture; any other is refused with KV_ERR_CAPTURE. */
 KV_API int kv_rotate_cached(kv_pool *pool, const kv_rotation *rotation, int32_t kv_type, const kv_shift *shifts, int32_t n,
                             int32_t layer_begin, int32_t layer_end, hipStream_t stream);
 

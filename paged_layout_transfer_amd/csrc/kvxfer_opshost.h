@@ -89,6 +89,13 @@ struct kv_attn_plan {
 
 namespace kvx {
 
+// Whether a token's keys, values and queries are as many as the kernels of rotations and of 4-bit appends count: eight tokens'
+// units of eight elements, and sixteen tokens' rows, in 31 bits.
+inline bool countable(const kv_pool_desc &d, int64_t q_heads, int64_t dim)
+{
+    return (2 * (int64_t)d.num_heads + q_heads) * dim <= 1 << 27;
+}
+
 // Whether the operators read and write pools of kv_type elements of such a shape; *dim is a head's width.
 inline int check_cache(const kv_pool_desc &d, int kv_type, int32_t *dim)
 {
@@ -96,6 +103,7 @@ inline int check_cache(const kv_pool_desc &d, int kv_type, int32_t *dim)
     if (!bytes && kv_type != KV_TYPE_F16 && kv_type != KV_TYPE_BF16) return KV_ERR_ARG;
     const int64_t wide = mx4 ? mx4_dim(d.head_dim) : d.head_dim;
     if (d.num_kv != 2 || d.elem_bytes != (bytes ? 1 : 2) || wide < 1 || wide > KV_MAX_ATTN_DIM) return KV_ERR_ARG;
+    if (mx4 && !countable(d, 0, wide)) return KV_ERR_ARG;
     if ((d.head_dim * d.elem_bytes) % (mx4 ? 4 : 16)) return KV_ERR_ALIGN;
     *dim = (int32_t)wide;
     return KV_OK;

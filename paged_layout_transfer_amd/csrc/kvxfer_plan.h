@@ -56,8 +56,9 @@ inline PlanLimits plan_limits(const kv_pool_desc &d, const kv_attn_desc &a)
     // a cut piece has two parts or more, and one record for KVX_JOIN_ROWS of its rows
     // of one piece (Split::across, mx4_pack)
     const int64_t heads_cut = l.mx4 ? std::min(l.heads, KVX_ROWS_FEW) : l.heads % 4 == 0 ? 4 : 1;
-    l.cap_groups = std::min(cut_few / 2 * heads_cut, few) *
-                   (l.mx4 ? std::min<int64_t>(rows, KVX_ROWS_FEW) : slices(std::min<int64_t>(rows, KVX_ROWS_FEW)));
+    l.cap_groups = std::min(cut_few / 2 * heads_cut, few) * slices(std::min<int64_t>(rows, KVX_ROWS_FEW));
+    // packs of more than KVX_JOIN_MANY parts: one for each row
+    if (l.mx4) l.cap_groups += std::min(cut_few / (KVX_JOIN_MANY + 1), few) * KVX_ROWS_FEW;
     l.cap_prows = cut_few * KVX_ROWS_FEW * (l.mx4 ? 1 : heads_cut);  // the heads of a pack share their 16 rows
     l.cap_many = 0;
     if (rows > KVX_ROWS_FEW) {

@@ -2,7 +2,9 @@
 // to other positions, cached tokens read back.  The exported functions are declared and documented in include/kvxfer.h.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
+#include <functional>
 #include <new>
 #include <vector>
 
@@ -112,6 +114,7 @@ int kv_append_rotated(kv_attn_plan *p, int32_t layer, const kv_rotation *rotatio
     AttnLaunch &a = r.attn;
     if (int rc = launch_base(p, layer, &a)) return rc;
     if (int rc = rotation_of(rotation, p->device, a.dim, &r.rot)) return rc;
+    if (!countable(p->pool->desc, rot->q ? p->desc.num_q_heads : 0, a.dim)) return KV_ERR_ARG;
     if (!p->plan.appendable || !scale_ok(p, x->k_scale) || !scale_ok(p, x->v_scale)) return KV_ERR_ARG;
     if (x->n_tokens < p->plan.tokens_end) return KV_ERR_RANGE;
     bool cap = false;
@@ -149,6 +152,7 @@ int kv_read_tokens(kv_attn_plan *p, int32_t layer_begin, int32_t layer_end, cons
     ReadLaunch r{};
     AttnLaunch &a = r.attn;
     if (int rc = launch_base(p, layer_begin, &a)) return rc;
+    if (!countable(d, 0, a.dim)) return KV_ERR_ARG;
     if (!p->plan.appendable || !scale_ok(p, x->k_scale) || !scale_ok(p, x->v_scale)) return KV_ERR_ARG;
     if (x->n_tokens < p->plan.tokens_end) return KV_ERR_RANGE;
     bool cap = false;
@@ -197,7 +201,7 @@ int kv_rotate_cached(kv_pool *p, const kv_rotation *rotation, int32_t kv_type, c
     if (layer_begin < 0 || layer_end > d.num_layers || layer_end <= layer_begin) return KV_ERR_ARG;
     ShiftLaunch a{};
     if (int rc = check_cache(d, kv_type, &a.dim)) return rc;
-    if (2 * rotation->pairs > a.dim) return KV_ERR_ARG;
+    if (2 * rotation->pairs > a.dim || !countable(d, 0, a.dim)) return KV_ERR_ARG;
     std::vector<ShiftRec> recs;
     int64_t items = 0;
     try {
@@ -213,6 +217,12 @@ int kv_rotate_cached(kv_pool *p, const kv_rotation *rotation, int32_t kv_type, c
             items += cdiv(s.t_end - s.t_begin, KVX_SHIFT_TOKENS);
             if (items > 0x7fffffffLL) return KV_ERR_ARG;
         }
+        std::vector<ShiftRec> by_place = recs;
+        std::sort(by_place.begin(), by_place.end(), [](const ShiftRec &a, const ShiftRec &b) {
+            return a.table != b.table ? std::less<const int32_t *>()(a.table, b.table) : a.begin < b.begin;
+        });
+        for (size_t i = 1; i < by_place.size(); ++i)
+            if (by_place[i].table == by_place[i - 1].table && by_place[i].begin < by_place[i - 1].end) return KV_ERR_DUP;
     } catch (...) {
         return KV_ERR_OOM;
     }

@@ -65,7 +65,10 @@ def shifts() -> None:
         return lib.kv_rotate_cached(h, ctypes.byref(no_rotation), kind, s, len(records) if n is None else n, *layers, None)
 
     assert call([]) == 0 and call([(None, 0, 5, 5, 1)]) == 0
-    assert call([(table, 64, 0, 1000, 7)] * 300) == A.KV_ERR_HIP      # all records taken, then no device
+    assert call([(table + 4096 * i, 64, 0, 1000, 7) for i in range(300)]) == A.KV_ERR_HIP     # all taken, then no device
+    assert call([(table, 64, 500, 1000, 7), (table, 64, 0, 500, 3)]) == A.KV_ERR_HIP           # side by side
+    assert call([(table, 64, 499, 1000, 7), (table + 64, 64, 0, 9, 1), (table, 64, 0, 500, 3)]) == A.KV_ERR_DUP
+    assert call([(table, 64, 0, 5, 7)] * 2) == A.KV_ERR_DUP
     for bad in ((None, 4, 0, 60, 1), (table + 2, 4, 0, 60, 1), (table, 3, 0, 60, 1), (table, 4, -1, 60, 1), (table, 4, 61, 60, 1),
                 (table, 2**31, 0, 60, 1), (table, 2**40, 0, 2**31, 1), (table, 2**62, 2**62, 2**63 - 1, 1)):
         assert call([(table, 64, 0, 10, 7), bad]) < 0
@@ -80,6 +83,11 @@ def shifts() -> None:
     assert lib.kv_rotate_cached(None, ctypes.byref(no_rotation), A.KV_TYPE_BF16, None, 0, 0, 1, None) < 0
     assert lib.kv_append_rotated(None, 0, None, None, None, None) < 0 and lib.kv_read_tokens(None, 0, 1, None, None) < 0
     assert lib.kv_pool_destroy(h) == 0
+    for heads, code in ((1 << 20, A.KV_ERR_HIP), (1 << 21, A.KV_ERR_ARG)):     # 2^27 elements of a token's k and v, 2^28
+        desc = A.make_pool_desc(1, 2, heads, 64, 2, 1, 64, heads * 128, [0x7F0000000000, 0x7F8000000000])
+        assert lib.kv_pool_create(ctypes.byref(desc), ctypes.byref(h)) == 0
+        assert call([(table, 64, 0, 10, 7)], layers=(0, 1)) == code
+        assert lib.kv_pool_destroy(h) == 0
 
 
 rows()

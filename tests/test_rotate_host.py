@@ -58,6 +58,7 @@ def _desc(heads=8, q=K.KV_TYPE_BF16, kv=K.KV_TYPE_MX4, seqs=4, tokens=64, window
     (dict(KV=1), dict(), K.KV_ERR_ARG),
     (dict(), dict(heads=3), K.KV_ERR_ARG),
     (dict(R=1 << 26, H=1, N=1, bs=1), dict(), K.KV_ERR_ARG),
+    (dict(R=68, H=1 << 20, N=1, bs=1), dict(heads=1 << 20, tokens=1), K.KV_ERR_ARG),    # 2^28 elements of a token
 ])
 def test_plan_refusals(pool, desc, code):
     p = _pool(**pool)
