@@ -252,6 +252,15 @@ struct ReadLaunch {
 // with one, 233 with two, 238 with four, 256 with eight).
 #define KVX_SHIFT_UNITS 8
 #define KVX_DEEP_GROUPS 1024  // workgroups that remain where one takes more than a layer
+#define KVX_SHIFT_GRID (1 << 20)  // workgroups along a shift's items at most
+
+// The items of one of a shift's workgroups: its own number, then every `step`-th below `end`.  Counted without a sign: an
+// item below 2^31 and a step of up to KVX_SHIFT_GRID may pass 31 bits together.
+struct ItemWalk {
+    uint32_t at, step, end;
+    KVX_HD bool there() const { return at < end; }
+    KVX_HD void next() { at += step; }
+};
 
 struct ShiftRec {
     const int32_t *table;

@@ -598,7 +598,8 @@ __global__ __launch_bounds__(kThreads) void shift_keys(const ShiftLaunch x)
                : (const KVX_CONST ShiftRec *)((const KVX_CONST uint8_t *)__builtin_amdgcn_kernarg_segment_ptr() + offsetof(ShiftLaunch, inl));
     const uint32_t pairs = x.rot.pairs;
     const int32_t layer0 = (int32_t)blockIdx.y * x.deep;
-    for (int32_t item = blockIdx.x; item < x.items; item += gridDim.x) {
+    for (ItemWalk walk{blockIdx.x, gridDim.x, (uint32_t)x.items}; walk.there(); walk.next()) {
+        const int32_t item = (int32_t)walk.at;
         int32_t r = 0, n = x.n;  // the last record that begins at or before the item
         while (n > 1) {
             const int32_t half = n >> 1;
@@ -761,7 +762,7 @@ int launch_shift(const ShiftLaunch &a, int kv_type, hipStream_t stream)
     set_div(units, &arg.unit_magic, &arg.unit_shift);
     set_div((uint32_t)a.heads, &arg.head_magic, &arg.head_shift);
     void *args[] = {&arg};
-    const uint32_t items = (uint32_t)std::min(a.items, 1 << 20);
+    const uint32_t items = (uint32_t)std::min(a.items, KVX_SHIFT_GRID);
     const int64_t own = ((int64_t)KVX_SHIFT_TOKENS * a.heads * units + kThreads - 1) / kThreads;
     arg.deep = layers_of(KVX_SHIFT_UNITS / own, a.items, a.layers);
     const uint32_t layers = (uint32_t)((a.layers + arg.deep - 1) / arg.deep);
