@@ -524,9 +524,9 @@ KV_API int kv_remap_tables(kv_pool *pool, const kv_page_copy *moves, int32_t n, 
  * half of byte b, 2b + 1 the high half: a sign bit over three bits of {0, 0.5, 1, 1.5, 2, 3, 4, 6} (OCP e2m1).  Scale
  * byte e stands for 2^(e - 127), 255 for NaN (OCP e8m0); an element is its value times its group's scale.  Transfers,
  * page copies, forks and compaction move such pools like any other.
- * What is written: the scale is the smallest power of two 2^s, s >= -126, with |x| <= 7 * 2^s for all
- * 32 values, and each element is x / 2^s rounded to nearest even and saturated at 6: values over 6 are off by
- * no more than others of their size, and the group keeps the finer scale.  A group that holds an infinity or NaN becomes NaN
+ * What is written: the scale is the smallest power of two 2^s, -126 <= s <= 127, with |x| <= 7 * 2^s for all
+ * 32 values (s is 127 where a turned key passes 7 * 2^127), and each element is x / 2^s rounded to nearest even and saturated
+ * at 6: values over 6 are off by no more than others of their size, and the group keeps the finer scale.  A group that holds an infinity or NaN becomes NaN
  * whole (scale byte 255, elements 0).  What is read is rounded to q_type (exact but for halves below 2^-24, and past the type's range).
  * kv_mx4_row_bytes: the smallest R for head_dim elements with which a token of num_heads rows is the multiple
  * of 16 bytes that a pool needs.  head_dim a multiple of 32 up to KV_MAX_ATTN_DIM (KV_ERR_ARG).

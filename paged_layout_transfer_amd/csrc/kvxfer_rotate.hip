@@ -9,7 +9,7 @@
 //
 // Keys on their way into an mx4 pool turn in 64 bits and are then rounded to 32 bits towards the odd neighbour, from which
 // the rounding to 4 bits gives the same as from all 64: so a stored value is that of the formula except where the formula
-// lies within 2^-45 or so of a border between two values.
+// lies within 2^-45 or so of a border between two values (2^-22 or so below 2^-126, where 32 bits hold fewer digits).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -125,10 +125,21 @@ __device__ __forceinline__ float to_odd(double x)
     return (float)__builtin_bit_cast(double, b);
 }
 
+// Turned values may pass the range of 32 bits, where a group's scale need not: such a group (its scale came out as that of an
+// infinity) is turned again at 2^-kDown of its size, values past what the largest scale holds cut to that, 7 * 2^127.
+// Infinities and NaN pass.
+static constexpr int kDown = 8;
+__device__ __forceinline__ float to_odd_cut(double x)
+{
+    constexpr double kMost = 7 * 0x1p119;
+    return to_odd(__builtin_fabs(x) < __builtin_inf() ? __builtin_fmin(__builtin_fmax(x, -kMost), kMost) : x);
+}
+
 // Eight consecutive values from element e on, turned in 64 bits: `x` themselves, `other` those that
 // are `pairs` away (only where halves are paired).
-template <bool ADJACENT>
-__device__ __forceinline__ void turn_wide(float (&x)[8], const float (&other)[8], uint32_t e, uint32_t pairs, const double2 *cs)
+template <bool ADJACENT, class Round>
+__device__ __forceinline__ void turn_wide(float (&x)[8], const float (&other)[8], uint32_t e, uint32_t pairs, const double2 *cs,
+                                          Round round)
 {
     if (ADJACENT) {
         if (e >= 2 * pairs) return;
@@ -136,8 +147,8 @@ __device__ __forceinline__ void turn_wide(float (&x)[8], const float (&other)[8]
         for (int i = 0; i < 4; ++i) {
             const double2 t = cs[e / 2 + i];
             const double u = x[2 * i], v = x[2 * i + 1];
-            x[2 * i] = to_odd(__builtin_fma(u, t.x, -(v * t.y)));
-            x[2 * i + 1] = to_odd(__builtin_fma(u, t.y, v * t.x));
+            x[2 * i] = round(__builtin_fma(u, t.x, -(v * t.y)));
+            x[2 * i + 1] = round(__builtin_fma(u, t.y, v * t.x));
         }
         return;
     }
@@ -151,7 +162,7 @@ __device__ __forceinline__ void turn_wide(float (&x)[8], const float (&other)[8]
             const double2 t = cs[(low ? at : at - pairs) + i];
             const double u = x[4 * h + i], v = other[4 * h + i];
             // the same products and sums as for the pair's other element's unit: x c - y s, x s + y c
-            x[4 * h + i] = to_odd(low ? __builtin_fma(u, t.x, -(v * t.y)) : __builtin_fma(v, t.y, u * t.x));
+            x[4 * h + i] = round(low ? __builtin_fma(u, t.x, -(v * t.y)) : __builtin_fma(v, t.y, u * t.x));
         }
     }
 }
@@ -391,10 +402,24 @@ __global__ __launch_bounds__(kThreads) void append_rotated(const AppendRotated x
                     values_of<T, 4>(other, o4[m][0]);
                     values_of<T, 4>(other + 4, o4[m][1]);
                 }
-                if (at.key) turn_wide<ADJACENT>(v, other, at.e, pairs, cs64[at.u]);
+                if (at.key) turn_wide<ADJACENT>(v, other, at.e, pairs, cs64[at.u], to_odd);
                 uint8_t *to = (at.key ? a.k_base : a.v_base) + place_of(a, pos0 + at.u, blk8[m]) + (int64_t)at.h * a.head_stride;
-                const uint32_t s = mx4_scale_of(v);
+                uint32_t s = mx4_scale_of(v), down = 0;
+                if (__builtin_expect(s == 255, 0)) {  // the same of the four lanes of a group
+                    const T *from = row_of(at, at.key, false);  // again: kept, it would take registers of every other group
+                    values_of<T, 8>(v, *(const T8 *)(from + at.e));
+                    if (at.key && !ADJACENT) {
+                        values_of<T, 4>(other, *(const T4 *)(from + partner(at.e, pairs)));
+                        values_of<T, 4>(other + 4, *(const T4 *)(from + partner(at.e + 4, pairs)));
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] *= 1.f / (1 << kDown), other[i] *= 1.f / (1 << kDown);
+                    if (at.key) turn_wide<ADJACENT>(v, other, at.e, pairs, cs64[at.u], to_odd_cut);
+                    s = mx4_scale_of(v);
+                    down = s == 255 ? 0 : kDown;
+                }
                 *(uint32_t *)(to + at.e / 2) = to_mx4(v, s);
+                s += down;
                 if (at.e % 32 == 0) to[a.dim / 2 + at.e / 32] = (uint8_t)s;
             }
             i0 += kAhead8 * kThreads;
@@ -585,8 +610,10 @@ int launch_read(const ReadLaunch &a, int q_type, int kv_type, uint32_t grid, hip
 // four rows in flight, segments of 8 or 16 bytes, items of 4, 8 or 16 tokens, pages in order and accesses past the caches;
 // a plain scale of as many bytes in place takes 198.  mx4 rows are bound by the vector pipe: 148 instructions for eight elements, 16
 // of them sums of 64 bits and 40 the roundings behind them; 32 layers of 2860 tokens of 2 heads, 25 MB, 23 us.
+// mx4: four waves a SIMD, as without the second turn of large groups; it costs 12 to 44 bytes of scratch, written and read once
+// an item, outside the loops (35.5 us with the read behind it, 35.2 without that turn).
 template <class T, int CACHE, bool ADJACENT, int VEC>
-__global__ __launch_bounds__(kThreads) void shift_keys(const ShiftLaunch x)
+__global__ __launch_bounds__(kThreads, CACHE == kMx4 ? 4 : 1) void shift_keys(const ShiftLaunch x)
 {
     constexpr bool MX4 = CACHE == kMx4;
     __shared__ float2 cs[MX4 ? 1 : kMaxPairs];
@@ -676,30 +703,61 @@ __global__ __launch_bounds__(kThreads) void shift_keys(const ShiftLaunch x)
                         w[m] = *(const uint32_t *)(row + e / 2);
                         scale[m] = row[x.dim / 2 + e / 32];
                     }
+                    float y[8];
+                    // A row's units lie in one wave, so a unit's partners come from the lanes that hold them.  WIDE: of
+                    // scales whose values 32 bits may not hold by 2^-kDown, and back in 64.
+                    auto turned = [&](uint32_t w, uint32_t scale, auto wide, auto round) __attribute__((always_inline)) {
+                        double v[8], other[8];
+                        auto values = [&](uint32_t w, uint32_t scale, double *to, int n) __attribute__((always_inline)) {
+                            const bool far = decltype(wide)::value && scale > 254 - kDown && scale < 255;
+                            const Vec<float>::x8 x = from_mx4<float>(w, mx4_scale(far ? scale - kDown : scale));
 #pragma unroll
-                    for (int m = 0; m < kRows * kLayers; ++m) {
-                        if (layer + m / kRows >= layer1) continue;
-                        // A row's units lie in one wave, so a unit's partners come from the lanes that hold them.
-                        Vec<float>::x8 v = from_mx4<float>(w[m], mx4_scale(scale[m])), other;
+                            for (int i = 0; i < n; ++i) to[i] = far ? (double)x[i] * (1 << kDown) : (double)x[i];
+                        };
+                        values(w, scale, v, 8);
                         if (ADJACENT) {
 #pragma unroll
                             for (int i = 0; i < 8; ++i) other[i] = e < 2 * pairs ? v[i ^ 1] : v[i];  // times 0 of its own sign
                         } else {
-                            const uint32_t w0 = __shfl(w[m], lane0), w1 = __shfl(w[m], lane1);
-                            const uint32_t s0 = __shfl(scale[m], lane0), s1 = __shfl(scale[m], lane1);
-                            const Vec<float>::x8 lo = from_mx4<float>(p0 % 8 ? w0 >> 16 : w0, mx4_scale(s0));
-                            const Vec<float>::x8 hi = from_mx4<float>(p1 % 8 ? w1 >> 16 : w1, mx4_scale(s1));
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) other[i] = lo[i], other[4 + i] = hi[i];
+                            const uint32_t w0 = __shfl(w, lane0), w1 = __shfl(w, lane1);
+                            const uint32_t s0 = __shfl(scale, lane0), s1 = __shfl(scale, lane1);
+                            values(p0 % 8 ? w0 >> 16 : w0, s0, other, 4);
+                            values(p1 % 8 ? w1 >> 16 : w1, s1, other + 4, 4);
                         }
-                        if (off[m % kRows] < 0) continue;
-                        float y[8];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) y[i] = to_odd(__builtin_fma((double)v[i], c[i], (double)other[i] * sn[i]));
-                        uint8_t *row = regions[2 * (m / kRows)] + off[m % kRows];
-                        const uint32_t s = mx4_scale_of(y);
+                        for (int i = 0; i < 8; ++i) y[i] = round(__builtin_fma(v[i], c[i], other[i] * sn[i]));
+                    };
+                    auto store = [&](uint8_t *row, uint32_t s, uint32_t down) __attribute__((always_inline)) {
                         *(uint32_t *)(row + e / 2) = to_mx4(y, s);
-                        if (j % 4 == 0) row[x.dim / 2 + j / 4] = (uint8_t)s;
+                        if (j % 4 == 0) row[x.dim / 2 + j / 4] = (uint8_t)(s + down);
+                    };
+                    uint32_t left = 0;  // rows of this wave with a group that came out as NaN: none of theirs is stored yet
+#pragma unroll
+                    for (int m = 0; m < kRows * kLayers; ++m) {
+                        if (off[m % kRows] < 0 || layer + m / kRows >= layer1) continue;
+                        turned(w[m], scale[m], std::false_type{}, to_odd);
+                        const uint32_t s = mx4_scale_of(y);
+                        if (__builtin_expect(__any(s == 255), 0)) left |= 1u << m;
+                        else store(regions[2 * (m / kRows)] + off[m % kRows], s, 0);
+                    }
+                    if (__builtin_expect(left != 0, 0)) {
+#pragma unroll 1
+                        for (int m = 0; m < kRows * kLayers; ++m) {
+                            if (!(left >> m & 1)) continue;
+                            int64_t at = off[0];
+#pragma unroll
+                            for (int k = 1; k < kRows; ++k) at = m % kRows == k ? off[k] : at;
+                            uint8_t *row = regions[2 * (m / kRows)] + at;
+                            const uint32_t again = *(const uint32_t *)(row + e / 2), scale = row[x.dim / 2 + e / 32];
+                            turned(again, scale, std::true_type{}, to_odd);
+                            uint32_t s = mx4_scale_of(y);
+                            const bool far = s == 255;  // the same of the four lanes of a group
+                            turned(again, scale, std::true_type{}, [&](double x) {
+                                return far ? to_odd_cut(x * (1. / (1 << kDown))) : to_odd(x);
+                            });
+                            s = mx4_scale_of(y);
+                            store(row, s, far && s < 255 ? kDown : 0);
+                        }
                     }
                 } else {
                     // only the units that turn

@@ -1,0 +1,78 @@
+"""Rotated appends, shifts and reads at the ends of their ranges on the GPU, against the same plain 64-bit implementations
+as tests/test_gpu_rotate.py.  Every case is printed before its first launch."""
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import rotated_reference as rot
+from paged_layout_transfer_amd import kvxfer as K
+from rotated_harness import TYPES, Cache, deal, frequencies, say, seqs_of
+from test_gpu_rotate import SPECIAL, append_case, shift_case
+
+pytestmark = pytest.mark.gpu
+
+MOST = 7 * 2.0 ** 127       # what the largest scale holds; turned keys may pass it, and are cut to it
+
+
+@pytest.fixture
+def cut(monkeypatch):
+    """The 4-bit reference with finite values cut to the largest scale's."""
+    plain = rot.mx4_of
+    monkeypatch.setattr(rot, "mx4_of", lambda x: plain(torch.where(torch.isfinite(x), x.double().clamp(-MOST, MOST), x.double())))
+
+
+# ---- 4-bit groups that a turn makes larger than 32 bits hold ------------------------------------
+
+@pytest.mark.parametrize("adjacent", [False, True], ids=["halves", "adjacent"])
+@pytest.mark.parametrize("amplitude", [1.0, 1.5, 2.0 ** 20, 3e38])
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+def test_turned_keys_past_the_range_of_32_bits(kind, amplitude, adjacent, cut):
+    """Keys up to the type's largest in groups with small and zero ones, infinities and NaN in others: 4-bit rows bit by bit."""
+    lens = [(40, 43)]
+    gen = torch.Generator().manual_seed(6)
+    most = torch.finfo(TYPES[kind]).max
+    x = torch.randn((43, 4 + 2 * 2, 64), generator=gen) * (most / 3)
+    x[::3] *= torch.exp2(-torch.randint(0, 20, x[::3].shape, generator=gen).float())
+    x[1::5, :, :32] = most
+    x[2::5, :, 32:] = -most
+    x[3, :, 7], x[8, :, 40], x[13, :, 0] = math.inf, -math.inf, math.nan
+    x[18:20, :, ::2] = 0.0
+    x = x.clamp(-most, most).to(TYPES[kind])
+    x[3, :, 7], x[8, :, 40] = math.inf, -math.inf
+    with Cache(heads=2, dim=64, blocks=8, kind=kind) as c:
+        append_case(c, lens, 4, frequencies(32), adjacent=adjacent, amplitude=float(np.float32(amplitude)), x=x, with_q=False)
+
+
+@pytest.mark.parametrize("pairs", [32, 12])
+@pytest.mark.parametrize("adjacent", [False, True], ids=["halves", "adjacent"])
+@pytest.mark.parametrize("top", [251, 252, 253, 254])
+def test_shifts_of_the_largest_scales(top, adjacent, pairs, cut):
+    """Groups up to each of the largest scales, whose values or whose turned values 32 bits do not hold, and NaN groups."""
+    with Cache(layers=2, heads=3, dim=64, page=16, blocks=12, gain=2.0 ** (top - 127)) as c:
+        c.view(0)[3, 5, 1, 32] = 255
+        c.view(2)[:, ::7, 0, 33] = 255
+        c.view(0)[:, 1::7, :, 32] = 0
+        c.upload()
+        shift_case(c, [(0, 61, 5), (3, 4, -77777), (7, 40, 2 ** 31 - 1), (0, 16, 0)], frequencies(pairs), adjacent, (0, 2))
+
+
+@pytest.mark.parametrize("adjacent", [False, True], ids=["halves", "adjacent"])
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+def test_special_values_of_a_turned_group(kind, adjacent, cut):
+    """The groups at the edges of the format, as keys that turn."""
+    extra = [[2.0 ** -126 * i for i in range(32)], [3e38, -3e38] + [1e37] * 30, [2.0 ** 100] * 32,
+             [3.3e38] * 32, [3.3e38 * (-1) ** i for i in range(32)]] if kind == "bf16" else []
+    groups = torch.tensor(SPECIAL + extra)
+    rows = len(groups)
+    x = torch.zeros(rows + 3, 6, 64)
+    x[:rows, 2, :32], x[:rows, 2, 32:] = groups, groups.flip(0)
+    x[:rows, 3, :32], x[:rows, 3, 32:] = groups.flip(0), groups * 0.5
+    x[:rows, 4], x[:rows, 5] = x[:rows, 2].flip(1), x[:rows, 3].flip(1)
+    x = x.to(TYPES[kind])
+    for pairs in (32, 16, 4):
+        with Cache(heads=2, dim=64, blocks=8, kind=kind) as c:
+            append_case(c, [(rows, rows + 3)], 2, frequencies(pairs), adjacent=adjacent, x=x, with_q=False)
