@@ -596,7 +596,7 @@ KV_API int kv_attend(kv_attn_plan *plan, int32_t layer, const kv_attend_args *ar
 /* Position rotation.  A token at position p turns pair i of a head by p * inv_freq[i]: of the pair's elements
  * (x, y) it makes amplitude * (x cos - y sin, x sin + y cos); elements from 2 * pairs on stay as they are.  Angles
  * are taken as fractions of a turn in 64 bits, p times inv_freq[i] / 2 pi rounded to 2^-64, so that they are
- * good to |p| 2^-64 turns at any position.  Products and sums are held in 32 bits, in 64 for keys on their
+ * good to |p| 2^-64 turns at any position (and to 2^-22 of themselves where sums are held in 32 bits).  Products and sums are held in 32 bits, in 64 for keys on their
  * way into a KV_TYPE_MX4 pool, and rounded once to what is written.
  * create copies the frequencies to the current device, where the rotation is then used, and waits for the
  * copy (KV_ERR_HIP while a stream captures); KV_ERR_ARG for pairs not 1 .. KV_MAX_ATTN_DIM / 2, an unknown

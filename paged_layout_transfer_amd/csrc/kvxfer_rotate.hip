@@ -4,8 +4,9 @@
 // Mathematics.  Pair (x, y) of a head at position p becomes (x c - y s, x s + y c) with c + i s = amplitude
 // e^(2 pi i p f), f the turns of a pair in one position.  f is a fraction of 64 bits, so p f is an exact
 // product modulo one turn: position 2^31 is as good as position 1 to 2^-33 turns.  The fraction's two top
-// bits choose the quarter, and what is left of it, within an eighth of a turn of zero, goes through the power series of
-// sine and cosine: to x^9 and x^10 in 32 bits (2^-29 and 2^-32 beyond them), to x^15 and x^16 in 64.
+// bits choose the quarter, and what is left of it, all 62 bits, within an eighth of a turn of zero, goes through the power series of
+// sine and cosine: to x^9 and x^10 in 32 bits (2^-29 and 2^-32 beyond them), to x^15 and x^16 in 64.  The sine is good relative to
+// itself, so that pairs of the slowest frequencies turn by what they should.
 //
 // Keys on their way into an mx4 pool turn in 64 bits and are then rounded to 32 bits towards the odd neighbour, from which
 // the rounding to 4 bits gives the same as from all 64: so a stored value is that of the formula except where the formula
@@ -35,8 +36,10 @@ __device__ __forceinline__ void of_quarter(uint32_t quarter, F c, F s, F amplitu
 
 __device__ __forceinline__ float2 turn32(uint64_t turns, float amplitude)
 {
-    const uint32_t t = (uint32_t)(turns >> 32), quarter = (t + 0x20000000u) >> 30;
-    const float x = (float)(int32_t)(t - (quarter << 30)) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+    // two words with signs of their own, the upper one rounded: small angles of either sign lie in the lower one whole
+    const uint32_t t = (uint32_t)((turns + 0x80000000u) >> 32), quarter = (t + 0x20000000u) >> 30;
+    const float rest = __builtin_fmaf((float)(int32_t)(uint32_t)turns, 0x1p-32f, (float)(int32_t)(t - (quarter << 30)));
+    const float x = rest * 1.4629180792671596e-9f;  // 2 pi / 2^32
     const float z = x * x;
     float s = __builtin_fmaf(z, 1.f / 362880, -1.f / 5040);
     s = __builtin_fmaf(z, s, 1.f / 120);

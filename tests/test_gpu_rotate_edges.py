@@ -10,7 +10,7 @@ import torch
 
 import rotated_reference as rot
 from paged_layout_transfer_amd import kvxfer as K
-from rotated_harness import TYPES, Cache, deal, frequencies, say, seqs_of
+from rotated_harness import KIND, TYPES, Cache, check_between, frequencies, round_to, say
 from test_gpu_rotate import SPECIAL, append_case, shift_case
 
 pytestmark = pytest.mark.gpu
@@ -76,3 +76,44 @@ def test_special_values_of_a_turned_group(kind, adjacent, cut):
     for pairs in (32, 16, 4):
         with Cache(heads=2, dim=64, blocks=8, kind=kind) as c:
             append_case(c, [(rows, rows + 3)], 2, frequencies(pairs), adjacent=adjacent, x=x, with_q=False)
+
+
+# ---- the slowest frequencies ---------------------------------------------------------------------
+
+@pytest.mark.parametrize("adjacent", [False, True], ids=["halves", "adjacent"])
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+def test_pairs_of_the_slowest_frequencies_turn(kind, adjacent):
+    """Pairs (x, 0): the second element becomes x sin a, good relative to itself.  Before the rounding to the type: the
+    frequency as a fraction of 64 bits (a half of 2^-64 turns of 1.6e-12 or more: 2^-25), the two parts of the rest, their sum and
+    its product with 2 pi / 2^32 (4 * 2^-24 with that constant's rounding), the series' last step and the product (2 * 2^-24):
+    under 2^-21 in all."""
+    n, t = 8, TYPES[kind]
+    freq = [1e-11, 3e-11, 1e-10, 7e-10, 1e-9, 2e-8, 5e-7, 3e-6] if kind == "bf16" else [3e-9, 1e-8, 2e-8, 1e-7, 3e-7, 1e-6, 3e-6, 1e-5]
+    first = list(range(0, 2 * n, 2)) if adjacent else list(range(n))
+    second = [i + 1 for i in first] if adjacent else [i + n for i in first]
+    gen = torch.Generator().manual_seed(8)
+    x = torch.zeros(60, 4, 32)
+    x[:, :, first] = (torch.rand((60, 4, n), generator=gen) + 1) * (1 if kind == "bf16" else 30000)
+    x = x.to(t)
+    pos = [int(p) for p in torch.randint(-300, 300, (60,), generator=gen)]
+    pos[:4] = [1, -1, 2, 0]
+    with Cache(heads=1, dim=32, blocks=8, kind=kind, cache=kind) as c:
+        table = torch.arange(8, dtype=torch.int32).cuda()
+        plan, r = c.plan(2, 1, 60), c.rotation(freq, adjacent)
+        K.kv_attn_plan_set(plan, K.make_seqs([(table, 8, 60, 0, 60)]), None)
+        x_d, pos_d = x.cuda(), torch.tensor(pos, dtype=torch.int32).cuda()
+        out, k, moved = (torch.zeros(60, h, 32, dtype=t, device="cuda") for h in (2, 1, 1))
+        torch.cuda.synchronize()
+        say("slow pairs", kind, "adjacent", adjacent)
+        K.kv_append_rotated(plan, 0, r, K.make_rotate_args(x_d[:, :2], out, pos_d),
+                            K.make_append_args(x_d[:, 2:3], x_d[:, 3:], n_tokens=60), None)
+        K.kv_read_tokens(plan, 0, 1, K.make_read_args(k, None, n_tokens=60), None)
+        K.kv_append_tokens(plan, 0, K.make_append_args(x_d[:, 2:3], x_d[:, 3:], n_tokens=60), None)
+        K.kv_rotate_cached(c.handle, r, KIND[kind], K.make_shifts([(table, 8, 0, 60, -3)]), 0, 1, None)
+        K.kv_read_tokens(plan, 0, 1, K.make_read_args(moved, None, n_tokens=60), None)
+        torch.cuda.synchronize()
+        for got, heads, at in ((out, slice(0, 2), pos), (k, slice(2, 3), pos), (moved, slice(2, 3), [-3])):
+            _, sn = rot.turned_by(at, freq)
+            y = x[:, heads][..., first].double() * sn[:, None]
+            a, b = round_to(y * (1 - 2.0 ** -21), t), round_to(y * (1 + 2.0 ** -21), t)
+            check_between(got.cpu()[..., second].double(), torch.minimum(a, b), torch.maximum(a, b), "x sin a")
