@@ -181,12 +181,19 @@ inline int append_rows(kv_attn_plan *p, const kv_append_args *x, AttnLaunch *a)
     return KV_OK;
 }
 
-// Whether no two elements of the array share memory (an output must not).
-inline bool apart(int64_t n, int32_t heads, int64_t token, int64_t head, int32_t dim)
+// Whether no two elements of the array share memory (an output must not): of its dimensions, in whichever order they lie,
+// each steps over all that the smaller ones span.
+inline bool apart(int64_t n, int32_t heads, int64_t token, int64_t head, int32_t dim, int64_t layers = 1, int64_t layer = 0)
 {
-    if (n <= 1 || heads <= 1) return (n <= 1 || token >= dim) && (heads <= 1 || head >= dim);
-    return token >= head ? head >= dim && token >= (heads - 1) * head + dim
-                         : token >= dim && head >= (n - 1) * token + dim;
+    std::pair<int64_t, int64_t> dims[3] = {{token, n}, {head, heads}, {layer, layers}};  // strides and counts
+    std::sort(dims, dims + 3);
+    int64_t span = dim;
+    for (const auto &[stride, count] : dims) {
+        if (count <= 1) continue;
+        if (stride < span) return false;
+        span += (count - 1) * stride;
+    }
+    return true;
 }
 
 inline bool scale_ok(const kv_attn_plan *p, float s)

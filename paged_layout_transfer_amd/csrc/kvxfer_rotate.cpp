@@ -167,12 +167,13 @@ int kv_read_tokens(kv_attn_plan *p, int32_t layer_begin, int32_t layer_end, cons
     for (const auto &t : to) {
         if (!t.rows) continue;
         if (int rc = check_rows(p, t.rows, x->n_tokens, d.num_heads, t.token, t.head)) return rc;
-        if (!apart(x->n_tokens, d.num_heads, t.token, t.head, a.dim)) return KV_ERR_ARG;
+        if (r.layers > 1) {
+            if (t.layer % 8) return KV_ERR_ALIGN;
+            if (t.layer < 0 || t.layer > INT64_MAX / 16 / r.layers) return KV_ERR_ARG;
+        }
+        if (!apart(x->n_tokens, d.num_heads, t.token, t.head, a.dim, r.layers, t.layer)) return KV_ERR_ARG;
         if (r.layers == 1) continue;
-        // the layers apart from each other: whole layers, one after another
-        if (t.layer % 8) return KV_ERR_ALIGN;
         const int64_t span = (x->n_tokens - 1) * t.token + (d.num_heads - 1) * t.head + a.dim;
-        if (t.layer < span || t.layer > INT64_MAX / 16 / r.layers) return KV_ERR_ARG;
         if (check_extent(p->extents, t.rows, 2 * ((r.layers - 1) * t.layer + span))) return KV_ERR_RANGE;
     }
     r.regions = p->pool->d_regions + 2 * (int64_t)layer_begin;

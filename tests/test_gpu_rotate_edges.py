@@ -10,7 +10,7 @@ import torch
 
 import rotated_reference as rot
 from paged_layout_transfer_amd import kvxfer as K
-from rotated_harness import KIND, TYPES, Cache, check_between, frequencies, round_to, say
+from rotated_harness import KIND, TYPES, Cache, check_between, deal, frequencies, round_to, say, seqs_of
 from test_gpu_rotate import SPECIAL, append_case, shift_case
 
 pytestmark = pytest.mark.gpu
@@ -117,3 +117,50 @@ def test_pairs_of_the_slowest_frequencies_turn(kind, adjacent):
             y = x[:, heads][..., first].double() * sn[:, None]
             a, b = round_to(y * (1 - 2.0 ** -21), t), round_to(y * (1 + 2.0 ** -21), t)
             check_between(got.cpu()[..., second].double(), torch.minimum(a, b), torch.maximum(a, b), "x sin a")
+
+
+# ---- reads into arrays of any order ------------------------------------------------------------------
+
+@pytest.mark.parametrize("store", ["bf16", "e4m3", "mx4"])
+@pytest.mark.parametrize("order", ["tlhd", "lthd", "thld", "hltd", "htld", "lhtd"])
+def test_reads_into_arrays_of_any_order(order, store):
+    """[tokens][layers][heads][dim] (the order of page-first chunks) and the others give what [layers][tokens][heads][dim]
+    gives, and leave what lies between untouched."""
+    lens, L, H, D = [(21, 21), (3, 40), (1, 1)], 3, 2, 64
+    with Cache(layers=L, heads=H, dim=D, blocks=8, cache=store) as c:
+        tables = [t.cuda() for t in deal(c, lens)]
+        seqs, rows = seqs_of(tables, lens)
+        plan = c.plan(H, len(lens), rows)
+        K.kv_attn_plan_set(plan, K.make_seqs(seqs), None)
+        n = rows + 2
+        plain = torch.full((2, L, n, H, D), 7.0, dtype=torch.bfloat16, device="cuda")
+        # k and v side by side, and eight elements to spare behind each
+        sizes = {"t": n, "l": L, "h": H, "d": D + 8}
+        both = torch.full([sizes[x] for x in order[:-1]] + [2, D + 8], 7.0, dtype=torch.bfloat16, device="cuda")
+        k, v = (both[..., i, :D].permute([order.index(x) for x in "lthd"]) for i in (0, 1))
+        torch.cuda.synchronize()
+        say("read", order, store)
+        scales = dict(n_tokens=n, k_scale=c.k_scale, v_scale=c.v_scale)
+        K.kv_read_tokens(plan, 0, L, K.make_read_args(plain[0], plain[1], **scales), None)
+        K.kv_read_tokens(plan, 0, L, K.make_read_args(k, v, k_strides=k.stride()[:3], v_strides=v.stride()[:3], **scales), None)
+        assert K.kv_pool_get_error(c.handle) == 0
+        assert torch.equal(k, plain[0]) and torch.equal(v, plain[1]) and not (plain[:, :, :rows] == 7).all()
+        assert (both[..., D:] == 7).all()
+
+
+def test_reads_into_arrays_that_overlap_are_refused():
+    with Cache(layers=2, heads=2, dim=64, blocks=8) as c:
+        table = torch.zeros(4, dtype=torch.int32, device="cuda")
+        plan = c.plan(2, 1, 8)
+        K.kv_attn_plan_set(plan, K.make_seqs([(table, 4, 8, 0, 8)]), None)
+        x = torch.zeros(8, 2, 2, 64, dtype=torch.bfloat16, device="cuda")
+        say("overlapping reads")
+        # (layer, token, head): a layer within a head's step, within a token's, on the heads, behind its own start, nowhere
+        for strides, code in (((64, 256, 64), K.KV_ERR_ARG), ((192, 256, 64), K.KV_ERR_ARG), ((56, 256, 64), K.KV_ERR_ARG),
+                              ((-128, 256, 64), K.KV_ERR_ARG), ((0, 256, 64), K.KV_ERR_ARG), ((132, 256, 64), K.KV_ERR_ALIGN),
+                              ((1 << 40, 256, 64), K.KV_ERR_RANGE), ((1 << 60, 256, 64), K.KV_ERR_ARG)):
+            with pytest.raises(K.KvError) as e:
+                K.kv_read_tokens(plan, 0, 2, K.make_read_args(x, None, n_tokens=8, k_strides=strides), None)
+            assert e.value.code == code, strides
+        K.kv_read_tokens(plan, 0, 2, K.make_read_args(x, None, n_tokens=8, k_strides=(128, 256, 64)), None)
+        K.kv_read_tokens(plan, 0, 2, K.make_read_args(x, None, n_tokens=8, k_strides=(64, 256, 128)), None)

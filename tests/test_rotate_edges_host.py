@@ -23,3 +23,8 @@ def _run_cpp(name, tmp_path):
 def test_shifts_of_as_many_items_as_a_call_may_have_end(tmp_path):
     """tests/shift_walk.cpp: a workgroup's last step passes 31 bits."""
     _run_cpp("shift_walk", tmp_path)
+
+
+def test_arrays_in_any_order_of_their_dimensions_are_taken(tmp_path):
+    """tests/apart_walk.cpp: outputs of layers, tokens and heads."""
+    _run_cpp("apart_walk", tmp_path)
