@@ -560,7 +560,7 @@ KV_API int kv_attn_plan_set(kv_attn_plan *plan, const kv_seq *seqs, int32_t n, h
 
 /* Writes the new tokens' k and v rows into their pages of one layer: the token at position p
  * goes to slot p % block_size of block block_table[p / block_size].  An e4m3 pool gets
- * x / scale, rounded to nearest even and saturated at +-448; NaN stays NaN; a KV_TYPE_MX4 pool gets rows as
+ * x / scale (in 32 bits), rounded to nearest even and saturated at +-448; NaN stays NaN; a KV_TYPE_MX4 pool gets rows as
  * above.  Nothing else is written, and rows of no sequence are not read.  Two sequences must not write one pool token.  A block id
  * out of range is skipped and reported (kv_pool_get_error).  Errors: KV_ERR_ARG (layer, null or
  * negative arguments, scales, a sequence with q_len > kv_len, another device current),
@@ -596,8 +596,9 @@ KV_API int kv_attend(kv_attn_plan *plan, int32_t layer, const kv_attend_args *ar
 /* Position rotation.  A token at position p turns pair i of a head by p * inv_freq[i]: of the pair's elements
  * (x, y) it makes amplitude * (x cos - y sin, x sin + y cos); elements from 2 * pairs on stay as they are.  Angles
  * are taken as fractions of a turn in 64 bits, p times inv_freq[i] / 2 pi rounded to 2^-64, so that they are
- * good to |p| 2^-64 turns at any position (and to 2^-22 of themselves where sums are held in 32 bits).  Products and sums are held in 32 bits, in 64 for keys on their
- * way into a KV_TYPE_MX4 pool, and rounded once to what is written.
+ * good to |p| 2^-64 turns at any position (and to 2^-22 of themselves where sums are held in 32 bits).  Products, sums and
+ * quotients are held in 32 bits, each rounded to them, in 64 for keys on their way into a KV_TYPE_MX4 pool; the result is then
+ * rounded to what is written.
  * create copies the frequencies to the current device, where the rotation is then used, and waits for the
  * copy (KV_ERR_HIP while a stream captures); KV_ERR_ARG for pairs not 1 .. KV_MAX_ATTN_DIM / 2, an unknown
  * pairing, or frequencies or an amplitude out of range, KV_ERR_ALIGN for pairs no multiple of 4.  destroy waits for the device
@@ -607,7 +608,7 @@ KV_API int kv_rotation_destroy(kv_rotation *rotation);
 
 /* kv_append_tokens with the rotation applied on the way, one launch: the new tokens' k rows are rotated, each to its
  * position, and written to their pages with the v rows; their q rows are rotated into q_out.  Rotated
- * values are rounded once, to the pool's type (after the division by k_scale) or q_type.  positions[row] is a
+ * values are rounded to the pool's type (e4m3: the quotient by k_scale, in 32 bits) or q_type.  positions[row] is a
  * token's position, of either sign; NULL takes its place in the cache.  Rows of no sequence are neither read
  * nor written.  q_out may be q with its strides; otherwise it overlaps nothing that the call reads.
  * Errors and capture as kv_append_tokens; also KV_ERR_ARG for a rotation wider than head_dim or of another
@@ -617,8 +618,8 @@ KV_API int kv_append_rotated(kv_attn_plan *plan, int32_t layer, const kv_rotatio
                              const kv_append_args *args, hipStream_t stream);
 
 /* The inverse of append: the new tokens' places in the cache of layers [layer_begin, layer_end), read as
- * q_type rows: 16-bit pools' rows as they are, k_scale or v_scale times an e4m3 element, KV_TYPE_MX4 rows' values, each
- * rounded once.  A plan whose sequences have q_len = kv_len reads caches whole.  Rows of no sequence, and of tokens
+ * q_type rows: 16-bit pools' rows as they are, k_scale or v_scale times an e4m3 element in 32 bits, KV_TYPE_MX4 rows' values,
+ * each then rounded.  A plan whose sequences have q_len = kv_len reads caches whole.  Rows of no sequence, and of tokens
  * whose block id is out of range (reported), are left as they were.  One launch.  Errors and capture as
  * kv_append_tokens; also KV_ERR_ARG for an empty layer range, no array at all, rows of an array that
  * overlap (layers, tokens and heads may lie in any order, each stride over all that the smaller ones span), and a token's

@@ -164,3 +164,30 @@ def test_reads_into_arrays_that_overlap_are_refused():
             assert e.value.code == code, strides
         K.kv_read_tokens(plan, 0, 2, K.make_read_args(x, None, n_tokens=8, k_strides=(128, 256, 64)), None)
         K.kv_read_tokens(plan, 0, 2, K.make_read_args(x, None, n_tokens=8, k_strides=(64, 256, 128)), None)
+
+
+# ---- the arithmetic of e4m3 reads ----------------------------------------------------------------------
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("scale", [0.037, 1.0, 1.2345678e-3, 3.0e4])
+def test_e4m3_elements_are_read_as_a_32_bit_product_rounded(kind, scale):
+    """Every e4m3 code, bit by bit (NaN as NaN)."""
+    with Cache(heads=2, dim=64, page=16, blocks=4, kind=kind, cache="e4m3") as c:
+        codes = torch.arange(256, dtype=torch.uint8)
+        c.bytes.view(2, -1)[:] = codes.repeat(c.bytes[0].numel() // 256)
+        c.upload()
+        table = torch.arange(4, dtype=torch.int32).cuda()
+        plan = c.plan(2, 1, 64)
+        K.kv_attn_plan_set(plan, K.make_seqs([(table, 4, 64, 0, 64)]), None)
+        k, v = (torch.zeros(64, 2, 64, dtype=TYPES[kind], device="cuda") for _ in range(2))
+        torch.cuda.synchronize()
+        say("e4m3 read", kind, scale)
+        K.kv_read_tokens(plan, 0, 1, K.make_read_args(k, v, n_tokens=64, k_scale=scale, v_scale=scale / 3), None)
+        torch.cuda.synchronize()
+        values = codes.view(torch.float8_e4m3fn).float().repeat(32)
+        for got, by in ((k, scale), (v, scale / 3)):
+            want = (values * torch.tensor(by, dtype=torch.float32)).to(TYPES[kind])
+            got = got.cpu().flatten()
+            assert torch.equal(torch.isnan(got), torch.isnan(want))
+            fine = ~torch.isnan(want)
+            assert torch.equal(got[fine].view(torch.int16), want[fine].view(torch.int16))
