@@ -298,7 +298,7 @@ typedef struct {
 typedef struct {
     int32_t pairs;          /* n, a multiple of 4 up to KV_MAX_ATTN_DIM / 2: the first 2n elements of a head turn */
     int32_t pairing;        /* KV_ROT_HALVES or KV_ROT_ADJACENT */
-    float amplitude;        /* of the turned elements, finite, > 0; 1 for a plain rotation */
+    float amplitude;        /* of the turned elements, finite, > 0; 1 for a plain rotation.  The formula takes these 32 bits */
     const double *inv_freq; /* host array of n angles a position turns pair i by, in radians, 0 .. 2^20 */
 } kv_rotation_desc;
 

@@ -9,8 +9,9 @@
 // itself, so that pairs of the slowest frequencies turn by what they should.
 //
 // Keys on their way into an mx4 pool turn in 64 bits and are then rounded to 32 bits towards the odd neighbour, from which
-// the rounding to 4 bits gives the same as from all 64: so a stored value is that of the formula except where the formula
-// lies within 2^-45 or so of a border between two values (2^-22 or so below 2^-126, where 32 bits hold fewer digits).
+// the rounding to 4 bits gives the same as from all 64: so a stored value is that of the formula, with the amplitude's 32
+// bits, except where the formula lies within 2^-45 or so of a border between two values (2^-22 or so below 2^-126, where 32 bits
+// hold fewer digits).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -191,3 +191,17 @@ def test_e4m3_elements_are_read_as_a_32_bit_product_rounded(kind, scale):
             assert torch.equal(torch.isnan(got), torch.isnan(want))
             fine = ~torch.isnan(want)
             assert torch.equal(got[fine].view(torch.int16), want[fine].view(torch.int16))
+
+
+# ---- amplitudes of 4-bit appends -------------------------------------------------------------------------
+
+@pytest.mark.parametrize("adjacent", [False, True], ids=["halves", "adjacent"])
+@pytest.mark.parametrize("amplitude", [1.0948, 0.7071, 3.0e-3])
+@pytest.mark.parametrize("shape", [(8, 2, 128, 64), (3, 3, 96, 20), (5, 1, 256, 128)])
+def test_4_bit_appends_with_an_amplitude(shape, amplitude, adjacent):
+    """Bit by bit, the amplitude as the 32-bit number that the descriptor holds."""
+    heads_q, heads, dim, pairs = shape
+    lens = [(5, 21), (0, 9), (1, 1), (33, 33), (8, 24)]
+    for kind in ("bf16", "f16"):
+        with Cache(heads=heads, dim=dim, blocks=20, kind=kind, pad=32) as c:
+            append_case(c, lens, heads_q, frequencies(pairs, 500000.0), adjacent=adjacent, amplitude=float(np.float32(amplitude)))
