@@ -5,8 +5,6 @@
 
 namespace kvx {
 
-// Keys of steps past the wave's last: no row sees them.
-#define KVX_NO_KEY 0x7fffff00
 // The scale bytes from which on some elements are infinite or NaN as T: 4 * 2^126 and 4 * 2^14 are past the types' ranges.
 template <class T>
 constexpr uint32_t mx4_not_finite() { return __is_same(T, __bf16) ? 127 + 126 : 127 + 14; }
