@@ -438,8 +438,10 @@ __device__ __forceinline__ void finish_few(const AttnLaunch &a, const Piece &s, 
 // bf16 heads, 4 query heads to a cache head: 32 sequences of 1 K to 64 K tokens 306 us, 5.7 TB/s;
 // one of 32 K 28 us and 6 us to join; a context that one step of each wave covers 7 us, the latency of
 // record, block id, rows and the way out.
+// 64-wide e4m3 heads keep four waves a SIMD, 128 registers, in all forms: 128 sequences of 4 K to 5.4 K, head-major, a cap of
+// 30 117 us (three waves, with 131 registers: 154), of 300 120 us (151).
 template <class T, int CACHE, int DP, int SHAPED>
-__global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_few(const AttnLaunch a)
+__global__ __launch_bounds__(256, DP == 256 ? 1 : CACHE == kE4m3 && DP == 64 ? 4 : 2) void attend_few(const AttnLaunch a)
 {
     typedef typename Vec<T>::x8 T8;
     typedef typename Vec<T>::x4 T4;
