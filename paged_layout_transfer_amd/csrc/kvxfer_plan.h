@@ -1,8 +1,8 @@
 // kvxfer_plan.h -- host planning of one step's attention: which pieces of work there are
 // and how they are split over the keys (host only; no HIP call; the vectors keep their
 // capacity, and std::stable_sort takes a buffer for the call).  On a host of the measured card a set takes 6 us for one
-// short decode, 9 for one on 32 K tokens, 17 for 16 sequences, 26 for 64 or for eight ragged turns, 53 for 256,
-// its upload's call included.
+// short decode, 7 for one on 32 K tokens, 11 for 16 sequences, 27 for 64 and for eight ragged turns, 60 for 256, its upload's
+// call included; over 4-bit pools 12, 29 and 65 for 16, 64 and 256, and with one and four new tokens in turn 12, 32 and 137.
 #pragma once
 #include <algorithm>
 #include <functional>
@@ -94,11 +94,18 @@ struct Plan {
     }
 };
 
+// How many of a piece there are beside the cache heads that all pieces are made for: an mx4 pool's sequences have packs of
+// different sizes where their rows differ, each a piece for every pack (AttnItem::across).
+struct Weight {
+    int32_t heads;  // of the pool; 0: one of each piece
+    int64_t operator()(const AttnItem &it) const { return heads ? heads / it.across : 1; }
+};
+
 // Parts that `share` tiles at most cut the pieces into, all cache heads together.
-inline int64_t parts_at(const std::vector<AttnItem> &whole, int64_t share, int32_t heads)
+inline int64_t parts_at(const std::vector<AttnItem> &whole, int64_t share, int32_t heads, Weight weight)
 {
     int64_t n = 0;
-    for (const AttnItem &it : whole) n += std::max<int64_t>(1, (it.tile1 + share - 1) / share);
+    for (const AttnItem &it : whole) n += std::max<int64_t>(1, (it.tile1 + share - 1) / share) * weight(it);
     return n * heads;
 }
 
@@ -118,27 +125,41 @@ constexpr SplitCost kCostFew{2, 2, 10, 2}, kCostMany{1, 4, 4, 8}, kCostHalf{1, 4
 // 2.1 us, 128-wide heads; 512 new tokens on 16 K cached, cut to one round either way: 217 and 155 us).
 constexpr int64_t kHalfTile = 72;
 
-// When the last of `slots` workgroups ends, in tiles, if each takes the longest part left.
-// `ends` is scratch.
-inline int64_t span_at(const std::vector<AttnItem> &whole, int64_t share, int64_t slots, const SplitCost &cost,
+// When the last of `slots` workgroups ends, in tiles, if each takes the longest part left.  Parts of one size go, and
+// workgroups that end at one time are kept, together, as tiles * 2^kRun + how many (no more parts than cut_parts()):
+// n parts of a piece have two sizes, and the packs of one sequence the same ones.  `parts` and `ends` are scratch.
+constexpr int kRun = 16;
+inline int64_t span_at(const std::vector<AttnItem> &whole, int64_t share, int64_t slots, const SplitCost &cost, Weight weight,
                        std::vector<int64_t> &parts, std::vector<int64_t> &ends)
 {
     parts.clear();
     bool any = false;
     for (const AttnItem &it : whole) {
-        const int64_t n = std::max<int64_t>(1, (it.tile1 + share - 1) / share);
+        const int64_t n = std::max<int64_t>(1, (it.tile1 + share - 1) / share), w = weight(it);
         any |= n > 1;
-        for (int64_t k = 0; k < n; ++k)
-            parts.push_back(it.tile1 * (k + 1) / n - it.tile1 * k / n + (n > 1 ? cost.cut : cost.whole));
+        const int64_t each = it.tile1 / n, less = each + (n > 1 ? cost.cut : cost.whole), more = it.tile1 - each * n;
+        if (more) parts.push_back(((less + 1) << kRun) + more * w);
+        parts.push_back((less << kRun) + (n - more) * w);
     }
     std::sort(parts.begin(), parts.end(), std::greater<int64_t>());
-    ends.assign((size_t)slots, 0);  // a heap, the earliest end first
-    for (int64_t p : parts) {
-        std::pop_heap(ends.begin(), ends.end(), std::greater<int64_t>());
-        ends.back() += p;
-        std::push_heap(ends.begin(), ends.end(), std::greater<int64_t>());
-    }
-    return *std::max_element(ends.begin(), ends.end()) + (any ? cost.join : 0);
+    ends.assign(1, slots);  // a heap, the earliest end first
+    int64_t last = 0;
+    for (const int64_t p : parts)
+        for (int64_t left = p & ((1 << kRun) - 1); left > 0;) {
+            std::pop_heap(ends.begin(), ends.end(), std::greater<int64_t>());
+            int64_t &e = ends.back();
+            const int64_t count = e & ((1 << kRun) - 1), taken = std::min(left, count), end = (e >> kRun) + (p >> kRun);
+            last = std::max(last, end);
+            left -= taken;
+            e -= taken;
+            if (taken < count) {
+                std::push_heap(ends.begin(), ends.end(), std::greater<int64_t>());
+                ends.push_back(0);
+            }
+            ends.back() = (end << kRun) + taken;
+            std::push_heap(ends.begin(), ends.end(), std::greater<int64_t>());
+        }
+    return last + (any ? cost.join : 0);
 }
 
 // Splits the pieces in `whole` (tile0 = 0, tile1 = all tiles, one for all cache heads) over the keys.
@@ -156,24 +177,27 @@ struct Split {
     int32_t across;       // cache heads of a workgroup
 };
 inline Split choose_split(Plan &p, const PlanLimits &l, int64_t slots, const SplitCost &cost, bool few,
-                          int64_t parts_max = INT64_MAX)
+                          int64_t parts_max = INT64_MAX, Weight weight = {0})
 {
-    int64_t total = 0, longest = 1;
-    for (const AttnItem &it : p.whole)
-        total += (int64_t)it.tile1 * l.heads, longest = std::max<int64_t>(longest, it.tile1);
+    int64_t total = 0, longest = 1, n_whole = 0;
+    for (const AttnItem &it : p.whole) {
+        total += (int64_t)it.tile1 * l.heads * weight(it);
+        longest = std::max<int64_t>(longest, it.tile1);
+        n_whole += weight(it);
+    }
     // Four heads to a workgroup where they are neighbours in a page and there is work enough to
     // give every wave some steps of its head.
     const int32_t across = few && l.token_major && l.heads % 4 == 0 && total >= KVX_ACROSS * slots ? 4 : 1;
     const int32_t units = l.heads / across;
     total /= across;
     const int64_t even = std::max(cost.min_tiles, (total + slots - 1) / slots);
-    const int64_t pieces = (int64_t)p.whole.size() * units;
+    const int64_t pieces = n_whole * units;
     parts_max = std::min(parts_max, cut_parts(pieces, slots));
     auto fitting = [&](int64_t parts) {
         int64_t lo = std::min(cost.min_tiles, longest), hi = longest;
         while (lo < hi) {
             const int64_t mid = (lo + hi) / 2;
-            if (parts_at(p.whole, mid, units) <= parts) hi = mid;
+            if (parts_at(p.whole, mid, units, weight) <= parts) hi = mid;
             else lo = mid + 1;
         }
         return lo;
@@ -183,12 +207,12 @@ inline Split choose_split(Plan &p, const PlanLimits &l, int64_t slots, const Spl
         out.share = std::min(even, longest);
     } else {
         const int64_t lanes = std::max<int64_t>(1, slots / units);
-        const int64_t uncut = span_at(p.whole, longest, lanes, cost, p.parts, p.ends);
+        const int64_t uncut = span_at(p.whole, longest, lanes, cost, weight, p.parts, p.ends);
         out.span = uncut;
         int64_t best = (uncut * 19 + 19) / 20;  // a cut for less than a twentieth is not worth its risk
         auto consider = [&](int64_t s) {
-            if (s >= longest || parts_at(p.whole, s, units) > parts_max) return;
-            const int64_t span = span_at(p.whole, s, lanes, cost, p.parts, p.ends);
+            if (s >= longest || parts_at(p.whole, s, units, weight) > parts_max) return;
+            const int64_t span = span_at(p.whole, s, lanes, cost, weight, p.parts, p.ends);
             if (span < best) out.span = best = span, out.share = s;
         };
         for (int64_t rounds = 1; rounds * slots <= parts_max; ++rounds)
@@ -333,17 +357,16 @@ inline void build_plan(Plan &p, const PlanLimits &l, const kv_seq *seqs, int32_t
             for (const AttnItem &it : p.whole) tiles += (int64_t)it.tile1 * it.across;
             const int64_t most = tiles / ((int64_t)KVX_PACK_TILES * l.slots_few);
             if (most < KVX_ROWS_FEW) (void)pieces_of(p, l, seqs, n, true, KVX_ROWS_FEW, std::max<int64_t>(1, most));
-            // The split is chosen with a piece for each pack, or, where all packs are of one size, for each sequence's first
-            // and as many heads as packs (a plan of 16 sequences: 234 us of the host, 40).
+            // The split is chosen with each sequence's first pack: as many heads as packs where all packs are of one size,
+            // else the first for all of them.
             const int32_t across = p.whole[0].across;
             const bool same = std::all_of(p.whole.begin(), p.whole.end(), [&](const AttnItem &it) { return it.across == across; });
             PlanLimits packs = l;
             packs.heads = same ? l.heads / across : 1;
             packs.token_major = false;
-            if (same)
-                p.whole.erase(std::remove_if(p.whole.begin(), p.whole.end(), [](const AttnItem &it) { return it.head; }), p.whole.end());
-            const Split split = choose_split(p, packs, l.slots_few, kCostFew, true);
-            if (same) (void)pieces_of(p, l, seqs, n, true, KVX_ROWS_FEW, std::max<int64_t>(1, most));
+            p.whole.erase(std::remove_if(p.whole.begin(), p.whole.end(), [](const AttnItem &it) { return it.head; }), p.whole.end());
+            const Split split = choose_split(p, packs, l.slots_few, kCostFew, true, INT64_MAX, Weight{same ? 0 : l.heads});
+            (void)pieces_of(p, l, seqs, n, true, KVX_ROWS_FEW, std::max<int64_t>(1, most));
             cut_packs(p, l, split, &prow);
         } else {
             cut(p, p.few, l, KVX_ROWS_FEW, choose_split(p, l, l.slots_few, kCostFew, true), &prow);

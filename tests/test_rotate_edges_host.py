@@ -28,3 +28,8 @@ def test_shifts_of_as_many_items_as_a_call_may_have_end(tmp_path):
 def test_arrays_in_any_order_of_their_dimensions_are_taken(tmp_path):
     """tests/apart_walk.cpp: outputs of layers, tokens and heads."""
     _run_cpp("apart_walk", tmp_path)
+
+
+def test_the_split_search_counts_equal_parts_together(tmp_path):
+    """tests/plan_spans.cpp: the same spans as parts dealt one by one, and few runs for steps of unequal token counts."""
+    _run_cpp("plan_spans", tmp_path)
