@@ -196,7 +196,12 @@ __device__ __forceinline__ typename Run<T, N>::type run_of(const float *x)
     return v;
 }
 
-// A store of what no one reads soon enough to find it in a cache of 4 MB.
+// A store past the caches, of turned queries and of rows that were read: what lies in the caches stays there, and nothing is
+// written back when the kernel ends.  With whoever reads it next in the same measurement: a layer's append and attention of
+// 2048, 8192 and 16384 new tokens 89, 630 and 2293 us, queries through the caches 88, 630 and 2298; of 64 decode
+// steps 105.0 and 105.2; reads of 7874 tokens of a 4-bit pool with copies of them 95.4 and 94.3, of 32 layers of 4000 262
+// and 284.  New keys and values go through the caches, where the attention finds them: past them those layers take 92, 637 and
+// 2311 us, a decode step 104.9.
 template <class E, class V>
 __device__ __forceinline__ void store_past(E *to, V v)
 {
@@ -455,11 +460,11 @@ __global__ __launch_bounds__(kThreads) void append_rotated(const AppendRotated x
             uint8_t *to = (at.key ? a.k_base : a.v_base) + place_of(a, pos0 + at.u, blk[m]) + (int64_t)at.h * a.head_stride;
             if constexpr (CACHE == kE4m3) {
                 const float scale = at.key ? a.k_scale : a.v_scale;
-                store_past(to + unit.a, to_e4m3<VEC>(v, scale));
-                store_past(to + unit.b, to_e4m3<VEC>(v + VEC, scale));
+                *(typename Run<uint8_t, VEC>::type *)(to + unit.a) = to_e4m3<VEC>(v, scale);
+                *(typename Run<uint8_t, VEC>::type *)(to + unit.b) = to_e4m3<VEC>(v + VEC, scale);
             } else {
-                store_past((T *)to + unit.a, run_of<T, VEC>(v));
-                store_past((T *)to + unit.b, run_of<T, VEC>(v + VEC));
+                *(TV *)((T *)to + unit.a) = run_of<T, VEC>(v);
+                *(TV *)((T *)to + unit.b) = run_of<T, VEC>(v + VEC);
             }
         }
         i0 += kAhead * kThreads;
