@@ -247,9 +247,9 @@ struct ReadLaunch {
 #define KVX_INLINE_SHIFTS 64  // records that ride in the kernel arguments
 #define KVX_READ_DEEP 4       // layers that a workgroup reads (32 of 2860 tokens of 2 heads: 13.9 us with 1, 11.7, 12.9 with 16)
 #define KVX_SHIFT_TOKENS 16   // tokens of one workgroup's item
-// Units of work of a thread for which a workgroup takes more layers: of 2 heads' mx4 rows, two units to a thread and layer,
-// four layers (30.1 us with one, 25.0 with two, 23.2 with four or eight); of 8 heads' 16-bit rows, four, two (232 us
-// with one, 233 with two, 238 with four, 256 with eight).
+// Units of work of a thread for which a workgroup takes more layers of mx4 rows: of 2 heads, two units to a thread and layer,
+// four layers (30.1 us with one, 25.0 with two, 23.2 with four or eight).  Of other rows it takes one: 8 heads' 16-bit rows
+// 232 us, 234 with two, 238 with four, 256 with eight.
 #define KVX_SHIFT_UNITS 8
 #define KVX_DEEP_GROUPS 1024  // workgroups that remain where one takes more than a layer
 #define KVX_SHIFT_GRID (1 << 20)  // workgroups along a shift's items at most

@@ -615,9 +615,10 @@ int launch_read(const ReadLaunch &a, int q_type, int kv_type, uint32_t grid, hip
 
 // An item is up to 16 tokens of one record, in some layers (y).  All of a record's tokens turn by the same angles, so a
 // workgroup works them out once, with the places of its tokens, and then streams the rows through.
-// 16-bit rows are bound by HBM: 32 layers of 9000 tokens of 8 heads, 1.18 GB in place, 232 us (5.1 TB/s), the same with one, two or
-// four rows in flight, segments of 8 or 16 bytes, items of 4, 8 or 16 tokens, pages in order and accesses past the caches;
-// a plain scale of as many bytes in place takes 198.  mx4 rows are bound by the vector pipe: 148 instructions for eight elements, 16
+// 16-bit rows are bound by HBM: 32 layers of 9000 tokens of 8 heads, 1.18 GB in place, 232 us (5.1 TB/s), and 234 with four rows in
+// flight and two layers to a workgroup (neighbours paired 232 and 241, a quarter of the pairs 117 and 126; e4m3 121 and 124); segments of
+// 8 or 16 bytes, items of 4, 8 or 16 tokens, pages in order and accesses past the caches the same; a plain scale of as many bytes
+// in place takes 198.  mx4 rows are bound by the vector pipe: 148 instructions for eight elements, 16
 // of them sums of 64 bits and 40 the roundings behind them; 32 layers of 2860 tokens of 2 heads, 25 MB, 23 us.
 // mx4: four waves a SIMD, as without the second turn of large groups; it costs 12 to 44 bytes of scratch, written and read once
 // an item, outside the loops (35.5 us with the read behind it, 35.2 without that turn).
@@ -628,7 +629,7 @@ __global__ __launch_bounds__(kThreads, CACHE == kMx4 ? 4 : 1) void shift_keys(co
     __shared__ float2 cs[MX4 ? 1 : kMaxPairs];
     __shared__ double2 cs64[MX4 ? kMaxPairs : 1];
     __shared__ int64_t place[KVX_SHIFT_TOKENS];  // of each token, or -1
-    constexpr int kRows = MX4 ? 2 : 4, kLayers = MX4 ? 2 : 1;
+    constexpr int kRows = 2, kLayers = MX4 ? 2 : 1;
     const KVX_CONST ShiftRec *recs =
         x.recs ? (const KVX_CONST ShiftRec *)x.recs
                : (const KVX_CONST ShiftRec *)((const KVX_CONST uint8_t *)__builtin_amdgcn_kernarg_segment_ptr() + offsetof(ShiftLaunch, inl));
@@ -831,7 +832,7 @@ int launch_shift(const ShiftLaunch &a, int kv_type, hipStream_t stream)
     void *args[] = {&arg};
     const uint32_t items = (uint32_t)std::min(a.items, KVX_SHIFT_GRID);
     const int64_t own = ((int64_t)KVX_SHIFT_TOKENS * a.heads * units + kThreads - 1) / kThreads;
-    arg.deep = layers_of(KVX_SHIFT_UNITS / own, a.items, a.layers);
+    arg.deep = layers_of(kv_type == KV_TYPE_MX4 ? KVX_SHIFT_UNITS / own : 1, a.items, a.layers);
     const uint32_t layers = (uint32_t)((a.layers + arg.deep - 1) / arg.deep);
     const void *fn = a.rot.adjacent ? (vec == 8 ? shift_kernel<true, 8>(kv_type) : shift_kernel<true, 4>(kv_type))
                                     : (vec == 8 ? shift_kernel<false, 8>(kv_type) : shift_kernel<false, 4>(kv_type));
