@@ -12,7 +12,9 @@ one 131072-token request, 2 MiB chunks = 1 layer x 512 tokens) streamed through 
 pinned host staging ring in windows of whole layers, against the host link
 bandwidth measured in the same run by one large hipMemcpy each way.
 
-Prints one JSON line (see the "roofline", "cpu_baseline" and "host_path" keys).
+Prints one JSON line (see the "roofline", "cpu_baseline" and "host_path" keys), short enough to
+be found whole at the end of a log; everything measured goes to stderr before it, one JSON
+object after "details:".
 """
 from __future__ import annotations
 
@@ -454,6 +456,19 @@ def cpu_baseline(res):
                                     one["sample"], res["name"], one["bytes"] / 1e9, one["s"])))
     out.update(host_cpu())
     return out
+
+
+def contract_line(out):
+    """The line on stdout: the headline, its roofline and baseline whole, of the other legs the rates alone."""
+    keep = ("metric", "value", "unit", "n_gpus", "steps", "warmup", "ms_per_step", "higher_is_better", "scaling",
+            "vs_baseline", "dtype", "data", "config", "roofline", "cpu_baseline", "parity")
+    line = {k: out[k] for k in keep}
+    line["roofline"] = {k: v for k, v in out["roofline"].items() if k != "note"}
+    line["host_path"] = {d: {k: round(v[k], 4) for k in ("gbs", "link_gbs", "link_frac")}
+                         for d, v in (out.get("host_path") or {}).items() if isinstance(v, dict) and "link_frac" in v}
+    line["other_workloads_hbm_frac"] = {n: [v[d]["hbm_frac"] for d in ("gather", "scatter")]
+                                        for n, v in (out.get("other_workloads") or {}).items()}
+    return json.dumps(line)
 
 
 def direction_roofline(payload, each_ms):
@@ -1337,7 +1352,8 @@ def main():
         "layer_pipeline": pipeline,
         "pool_placement": placement,
     }
-    print(json.dumps(out), flush=True)
+    log("details: " + json.dumps(out))
+    print(contract_line(out), flush=True)
 
 
 if __name__ == "__main__":
