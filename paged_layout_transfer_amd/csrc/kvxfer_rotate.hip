@@ -318,10 +318,11 @@ struct AppendEight {
 // keys and values kAhead8) of them loaded by a thread before the first is turned.  An mx4 pool's keys and values, with angles
 // and sums of 64 bits, and the queries have workgroups of their own (blockIdx.y): the first loads of the former are on their
 // way while the angles are worked out.
-// Bound by HBM: 8192 new tokens of 32 heads on 8, 128 wide, 201 MB, in 33.6 us (6.0 TB/s); written through the caches 45 us.
-// Into an e4m3 pool the quotients' instructions count: 4326 tokens, 97 MB, 20.9 us.  Into an mx4 pool 7874 tokens, 169 MB, in
-// 31.1 us (5.4 TB/s); keys, values and queries in one workgroup after another: 36 us, and 5.7 us instead of 4.3 for the 16
-// tokens of a decode step.  Loads ahead of the angles of 32 bits cost registers and give nothing (33.6 -> 35.0 us).
+// Bound by HBM: 8192 new tokens of 32 heads on 8, 128 wide, 201 MB, in 34.7 us (5.8 TB/s); queries too through the caches 45 us.
+// Into an e4m3 pool the quotients' instructions count: 4326 tokens, 97 MB, 20.8 us.  Into an mx4 pool 7874 tokens, 169 MB, in
+// 31.6 us (5.3 TB/s); keys, values and queries in one workgroup after another: 36 us, and 5.7 us instead of 4.3 for the 16
+// tokens of a decode step.  Loads ahead of the angles of 32 bits cost registers and give nothing (33.6 -> 35.0 us, all stores
+// past the caches).
 template <class T, int CACHE, bool ADJACENT, int VEC>
 __global__ __launch_bounds__(kThreads) void append_rotated(const AppendRotated x)
 {
@@ -498,7 +499,7 @@ int launch_append_rotated(const AppendRotated &a, int q_type, int kv_type, uint3
     const uint32_t all = units * (uint32_t)l.heads * ((mx4 ? 0 : 2) + (l.q ? (uint32_t)l.group : 0));
     const uint32_t threads = std::max(all, mx4 ? 2 * eights * (uint32_t)l.heads : 0);
     // Angles of 64 bits, and 17 bytes written for 64 read: eight tokens to a workgroup where there are many (7874 tokens of 32
-    // heads on 8: 36.4 -> 31.1 us; of 16-bit pools 33.6 -> 35.4, e4m3 20.9 -> 24.0).
+    // heads on 8: 36.4 -> 31.1 us; of 16-bit pools 33.6 -> 35.4, e4m3 20.9 -> 24.0, all stores past the caches).
     arg.lg_split = mx4 && 2 * grid >= KVX_DEEP_GROUPS ? 0 : lg_split(threads);
     set_div(units, &arg.unit_magic, &arg.unit_shift);
     set_div(all ? all : 1, &arg.all_magic, &arg.all_shift);
@@ -618,8 +619,8 @@ int launch_read(const ReadLaunch &a, int q_type, int kv_type, uint32_t grid, hip
 // 16-bit rows are bound by HBM: 32 layers of 9000 tokens of 8 heads, 1.18 GB in place, 232 us (5.1 TB/s), and 234 with four rows in
 // flight and two layers to a workgroup (neighbours paired 232 and 241, a quarter of the pairs 117 and 126; e4m3 121 and 124); segments of
 // 8 or 16 bytes, items of 4, 8 or 16 tokens, pages in order and accesses past the caches the same; a plain scale of as many bytes
-// in place takes 198.  mx4 rows are bound by the vector pipe: 148 instructions for eight elements, 16
-// of them sums of 64 bits and 40 the roundings behind them; 32 layers of 2860 tokens of 2 heads, 25 MB, 23 us.
+// in place takes 198.  mx4 rows are bound by the vector pipe: 171 instructions to eight elements over a launch, 16
+// of them sums of 64 bits and 40 the roundings behind them; 32 layers of 2860 tokens of 2 heads, 25 MB, 23.6 us.
 // mx4: four waves a SIMD, as without the second turn of large groups; it costs 12 to 44 bytes of scratch, written and read once
 // an item, outside the loops (35.5 us with the read behind it, 35.2 without that turn).
 template <class T, int CACHE, bool ADJACENT, int VEC>
