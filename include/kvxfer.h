@@ -623,7 +623,7 @@ KV_API int kv_append_rotated(kv_attn_plan *plan, int32_t layer, const kv_rotatio
  * whose block id is out of range (reported), are left as they were.  One launch.  Errors and capture as
  * kv_append_tokens; also KV_ERR_ARG for an empty layer range, no array at all, rows of an array that
  * overlap (layers, tokens and heads may lie in any order, each stride over all that the smaller ones span), and a token's
- * k and v of more than 2^27 elements. */
+ * k and v of more than 2^27 elements.  The two arrays overlap neither each other nor the pool. */
 KV_API int kv_read_tokens(kv_attn_plan *plan, int32_t layer_begin, int32_t layer_end, const kv_read_args *args,
                           hipStream_t stream);
 
